@@ -82,6 +82,17 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.ent_entmax_rows_fwd.restype = ci
     lib.ent_entmax_rows_bwd.argtypes = [vp, vp, vp, ci, ci, ci, cf, vp, vp]
     lib.ent_entmax_rows_bwd.restype = ci
+    lib.ent_attn_kv4_write.argtypes = [vp, vp, ci, ci, ci, ci, ci, vp, ci, vp, vp, vp, vp, vp, vp,
+                                       ci, ci, vp, vp]
+    lib.ent_attn_kv4_write.restype = ci
+    lib.ent_attn_kv4_read.argtypes = [vp, vp, vp, vp, ci, ci, vp, ci, vp, vp, ci, ci, ci, ci, ci,
+                                      vp, vp, vp, vp]
+    lib.ent_attn_kv4_read.restype = ci
+    lib.ent_attn_kv4_workspace_size.argtypes = [ci] * 9
+    lib.ent_attn_kv4_workspace_size.restype = sz
+    lib.ent_attn_kv4_fwd.argtypes = [vp, ci, ci, ci, ci, ci, ci, cf, ci, ci, vp, vp, vp, vp, ci,
+                                     ci, vp, ci, vp, vp, ci, vp, vp, vp, vp, sz, vp]
+    lib.ent_attn_kv4_fwd.restype = ci
     _lib = lib
     return lib
 
@@ -186,3 +197,29 @@ def ent_attn_bwd_lists(q, k, v, list_key, list_u, list_n, dout, tau, block_mask,
     return load().ent_attn_bwd_lists(q, k, v, list_key, list_u, list_n, dout, tau, block_mask, B,
                                      H, N, d, dtype, float(alpha), int(causal), dq, dk, dv, ws,
                                      ws_bytes, stream)
+
+
+def ent_attn_kv4_write(k, v, B, Hkv, L, d, dtype, block_table, max_pages, start, new_lens, k_codes,
+                       k_meta, v_codes, v_meta, pages, page, bad, stream) -> int:
+    return load().ent_attn_kv4_write(k, v, B, Hkv, L, d, dtype, block_table, max_pages, start,
+                                     new_lens, k_codes, k_meta, v_codes, v_meta, pages, page, bad,
+                                     stream)
+
+
+def ent_attn_kv4_read(k_codes, k_meta, v_codes, v_meta, pages, page, block_table, max_pages, start,
+                      new_lens, B, Hkv, L, d, dtype, k, v, bad, stream) -> int:
+    return load().ent_attn_kv4_read(k_codes, k_meta, v_codes, v_meta, pages, page, block_table,
+                                    max_pages, start, new_lens, B, Hkv, L, d, dtype, k, v, bad,
+                                    stream)
+
+
+def ent_attn_kv4_workspace_size(B, Hq, Hkv, L, d, dtype, max_len, window, sinks) -> int:
+    return load().ent_attn_kv4_workspace_size(B, Hq, Hkv, L, d, dtype, max_len, window, sinks)
+
+
+def ent_attn_kv4_fwd(q, B, Hq, Hkv, L, d, dtype, alpha, window, sinks, k_codes, k_meta, v_codes,
+                     v_meta, pages, page, block_table, max_pages, start, new_lens, max_len, o, tau,
+                     bad, ws, ws_bytes, stream) -> int:
+    return load().ent_attn_kv4_fwd(q, B, Hq, Hkv, L, d, dtype, alpha, window, sinks, k_codes,
+                                   k_meta, v_codes, v_meta, pages, page, block_table, max_pages,
+                                   start, new_lens, max_len, o, tau, bad, ws, ws_bytes, stream)

@@ -649,3 +649,165 @@ extern "C" ent_status ent_attn_noalloc_read_status(long long* counters, void* st
                     "ent_attn_noalloc_read_status: no ent_attn_bwd_noalloc call on device %d yet", dev);
     return read_header(base, counters, stream);
 }
+
+// ---------------------------------------------------------------- 4-bit cache
+namespace {
+
+// Pool, block table and row counts of a call; fills a.g, a.Hkv, a.table, a.start, a.new_lens.
+ent_status check_kv4(ent::Kv4Args& a, const void* kc, const void* km, const void* vc, const void* vm,
+                     int pages, int page, const int32_t* table, int max_pages, const int32_t* start,
+                     const int32_t* new_lens, int B, int Hkv, int L, int d, int dtype, int32_t* bad) {
+    if (B < 0 || Hkv < 1 || L < 0) return fail(ENT_EINVAL, "bad size (B=%d Hkv=%d L=%d)", B, Hkv, L);
+    if (dtype != ENT_F32 && dtype != ENT_BF16) return fail(ENT_EINVAL, "unknown dtype %d", dtype);
+    if (d != 32 && d != 64 && d != 128)
+        return fail(ENT_EUNSUPPORTED, "head dim d=%d (supported: 32, 64, 128)", d);
+    if (page < ent::kKvTile || (page & (page - 1)) != 0)
+        return fail(ENT_EINVAL, "page of %d tokens (a power of two of at least %d)", page, ent::kKvTile);
+    if (pages < 0 || max_pages < 0) return fail(ENT_EINVAL, "negative size (pages=%d max_pages=%d)", pages, max_pages);
+    if ((long long)B * Hkv > 65535) return fail(ENT_EUNSUPPORTED, "B*Hkv=%lld exceeds 65535", (long long)B * Hkv);
+    if ((long long)max_pages * page > 1ll << 30)   // positions and chunk ends stay clear of 31 bits
+        return fail(ENT_EUNSUPPORTED, "max_pages * page = %lld tokens exceed 2^30", (long long)max_pages * page);
+    if ((long long)B * Hkv * L > 0x7fffffffll) return fail(ENT_EUNSUPPORTED, "B*Hkv*L exceeds 31 bits");
+    if (B > 0 && L > 0) {
+        if ((!table && max_pages > 0) || !start) return fail(ENT_EINVAL, "null block_table/start pointer");
+        if (pages > 0 && (!kc || !km || !vc || !vm)) return fail(ENT_EINVAL, "null cache pointer");
+        if (!aligned16(kc) || !aligned16(km) || !aligned16(vc) || !aligned16(vm))
+            return fail(ENT_EINVAL, "cache arrays must be 16-byte aligned");
+    }
+    a.g.B = B; a.g.L = L; a.g.pages = pages; a.g.max_pages = max_pages;
+    a.g.max_len = max_pages * page;
+    while ((1 << a.g.page_shift) < page) ++a.g.page_shift;
+    a.Hkv = Hkv;
+    a.group = 1;
+    a.table = table; a.start = start; a.new_lens = new_lens; a.bad = bad;
+    a.k_codes = static_cast<uint8_t*>(const_cast<void*>(kc));
+    a.v_codes = static_cast<uint8_t*>(const_cast<void*>(vc));
+    a.k_meta = const_cast<void*>(km);
+    a.v_meta = const_cast<void*>(vm);
+    return ENT_OK;
+}
+
+// Workspace of the attention: per row and chunk the maximum and the count, then the
+// candidates' scores and keys.  The rows of one key head share a scores CTA, 8, 16 or 32
+// of them (matrix instructions are 8 queries wide; float32 rows at d = 128 take two parts
+// each and stay at 16).
+struct Kv4Layout {
+    int ntile, chunk, nchunk;
+    size_t n, x, j, total;
+};
+
+bool kv4_layout(const ent::Kv4Geom& g, long long rows, int group, int d, int dtype, Kv4Layout* l) {
+    const long long per = (long long)g.L * group;
+    l->ntile = per <= 8 ? 1 : per <= 16 || (dtype == ENT_F32 && d == 128) ? 2 : 4;
+    if (per > 8ll * l->ntile * 65535 || rows > 0x7fffffffll) return false;
+    l->chunk = ent::kv4_chunk_keys(l->ntile);
+    l->nchunk = ent::kv4_chunks(g, l->chunk);
+    const size_t lists = (size_t)rows * l->nchunk;
+    l->n = round_up(lists * 4, 256);
+    l->x = l->n + round_up(lists * 4, 256);
+    l->j = l->x + round_up(lists * l->chunk * 4, 256);
+    l->total = l->j + round_up(lists * l->chunk * 2, 256);
+    return true;
+}
+
+ent_status check_kv4_attn(ent::Kv4Args& a, int Hq, int max_len, int window, int sinks, int d, int dtype,
+                          Kv4Layout* l) {
+    if (Hq < 1 || Hq % a.Hkv != 0) return fail(ENT_EINVAL, "Hq=%d is no multiple of Hkv=%d", Hq, a.Hkv);
+    if (window < 0 || sinks < 0) return fail(ENT_EINVAL, "negative window=%d or sinks=%d", window, sinks);
+    if (sinks > 0 && window == 0) return fail(ENT_EINVAL, "sinks=%d without a window", sinks);
+    if (max_len < 0) return fail(ENT_EINVAL, "negative max_len=%d", max_len);
+    a.group = Hq / a.Hkv;
+    a.g.max_len = max_len;
+    a.g.window = window;
+    a.g.sinks = sinks;
+    if (!kv4_layout(a.g, (long long)a.g.B * Hq * a.g.L, a.group, d, dtype, l))
+        return fail(ENT_EUNSUPPORTED, "B*Hq*L=%lld rows, %lld of one key head, are too many",
+                    (long long)a.g.B * Hq * a.g.L, (long long)a.g.L * a.group);
+    return ENT_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+ent_status ent_attn_kv4_write(const void* k, const void* v, int B, int Hkv, int L, int d, int dtype,
+                              const int32_t* block_table, int max_pages, const int32_t* start,
+                              const int32_t* new_lens, void* k_codes, void* k_meta, void* v_codes,
+                              void* v_meta, int pages, int page, int32_t* bad, void* stream) {
+    ent::Kv4Args a{};
+    ent_status st = check_kv4(a, k_codes, k_meta, v_codes, v_meta, pages, page, block_table, max_pages,
+                              start, new_lens, B, Hkv, L, d, dtype, bad);
+    if (st != ENT_OK) return st;
+    if (B == 0 || L == 0) return ENT_OK;
+    if (!k || !v) return fail(ENT_EINVAL, "null k/v pointer");
+    if (!aligned16(k) || !aligned16(v)) return fail(ENT_EINVAL, "k/v must be 16-byte aligned");
+    a.k = k; a.v = v;
+    cudaError_t e = ent::kv4_write(a, d, dtype == ENT_BF16, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ENT_OK : cuda_fail(e, "cache write launch");
+}
+
+ent_status ent_attn_kv4_read(const void* k_codes, const void* k_meta, const void* v_codes,
+                             const void* v_meta, int pages, int page, const int32_t* block_table,
+                             int max_pages, const int32_t* start, const int32_t* new_lens, int B,
+                             int Hkv, int L, int d, int dtype, void* k, void* v, int32_t* bad,
+                             void* stream) {
+    ent::Kv4Args a{};
+    ent_status st = check_kv4(a, k_codes, k_meta, v_codes, v_meta, pages, page, block_table, max_pages,
+                              start, new_lens, B, Hkv, L, d, dtype, bad);
+    if (st != ENT_OK) return st;
+    if (B == 0 || L == 0) return ENT_OK;
+    if (!k || !v) return fail(ENT_EINVAL, "null k/v pointer");
+    if (!aligned16(k) || !aligned16(v)) return fail(ENT_EINVAL, "k/v must be 16-byte aligned");
+    a.k_out = k; a.v_out = v;
+    cudaError_t e = ent::kv4_read(a, d, dtype == ENT_BF16, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ENT_OK : cuda_fail(e, "cache read launch");
+}
+
+size_t ent_attn_kv4_workspace_size(int B, int Hq, int Hkv, int L, int d, int dtype, int max_len,
+                                   int window, int sinks) {
+    if (B < 0 || Hkv < 1 || Hq < 1 || Hq % Hkv != 0 || L < 0 || max_len < 0 || window < 0 || sinks < 0 ||
+        (sinks > 0 && window == 0))
+        return 0;
+    ent::Kv4Geom g{};
+    g.B = B; g.L = L; g.max_len = max_len; g.window = window; g.sinks = sinks;
+    Kv4Layout l;
+    return kv4_layout(g, (long long)B * Hq * L, Hq / Hkv, d, dtype, &l) ? l.total : 0;
+}
+
+ent_status ent_attn_kv4_fwd(const void* q, int B, int Hq, int Hkv, int L, int d, int dtype,
+                            float alpha, int window, int sinks, const void* k_codes,
+                            const void* k_meta, const void* v_codes, const void* v_meta, int pages,
+                            int page, const int32_t* block_table, int max_pages,
+                            const int32_t* start, const int32_t* new_lens, int max_len, void* o,
+                            float* tau, int32_t* bad, void* ws, size_t ws_bytes, void* stream) {
+    ent::Kv4Args a{};
+    ent_status st = check_kv4(a, k_codes, k_meta, v_codes, v_meta, pages, page, block_table, max_pages,
+                              start, new_lens, B, Hkv, L, d, dtype, bad);
+    if (st != ENT_OK) return st;
+    if (!(alpha > 1.f && alpha <= 2.f)) return fail(ENT_EINVAL, "alpha=%g outside (1, 2]", (double)alpha);
+    if (max_len > a.g.max_len)
+        return fail(ENT_EINVAL, "max_len=%d exceeds max_pages * page = %d", max_len, a.g.max_len);
+    Kv4Layout l;
+    if ((st = check_kv4_attn(a, Hq, max_len, window, sinks, d, dtype, &l)) != ENT_OK) return st;
+    if (B == 0 || L == 0) return ENT_OK;
+    if (!q || !o) return fail(ENT_EINVAL, "null q/o pointer");
+    if (!aligned16(q) || !aligned16(o)) return fail(ENT_EINVAL, "q/o must be 16-byte aligned");
+    if (l.total > 0 && !ws) return fail(ENT_EINVAL, "null workspace");
+    if (ws_bytes < l.total)
+        return fail(ENT_EINVAL, "workspace of %zu bytes is below the required %zu", ws_bytes, l.total);
+    if (!aligned16(ws)) return fail(ENT_EINVAL, "workspace pointer not 16-byte aligned");
+    a.q = q; a.o = o; a.tau = tau;
+    a.alpha = alpha;
+    const int gm = gamma_mode(alpha, &a.gamma);
+    a.cx = (alpha - 1.f) / sqrtf((float)d);
+    a.ntile = l.ntile; a.chunk = l.chunk; a.nchunk = l.nchunk;
+    char* base = static_cast<char*>(ws);
+    a.chunk_max = reinterpret_cast<float*>(base);
+    a.chunk_n = reinterpret_cast<int*>(base + l.n);
+    a.cand_x = reinterpret_cast<float*>(base + l.x);
+    a.cand_j = reinterpret_cast<uint16_t*>(base + l.j);
+    cudaError_t e = ent::kv4_attn(a, d, dtype == ENT_BF16, gm, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ENT_OK : cuda_fail(e, "cache attention launch");
+}
+
+}  // extern "C"

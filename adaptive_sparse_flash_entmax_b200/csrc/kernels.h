@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 #include "common.cuh"
+#include "kv4_index.h"
 
 namespace ent {
 
@@ -115,6 +116,38 @@ struct RowArgs {
     float ftol, stol;      // stop rule, as in FwdArgs
 };
 cudaError_t rows_entmax(const RowArgs& a, int dtype_bf16, int gm, bool bwd, cudaStream_t s);
+
+// 4-bit key/value cache and the attention over it (kv4.cu); layouts in kv4_index.h.
+struct Kv4Args {
+    Kv4Geom g;
+    int Hkv, group;             // key/value heads, query heads per key head
+    const int* table;           // block table [B][max_pages]
+    const int* start;           // [B] position of row 0
+    const int* new_lens;        // [B] real rows, nullable: g.L
+    int* bad;                   // nullable: kKvBad* bits are or'ed in
+    uint8_t* k_codes;           // the pool
+    void* k_meta;
+    uint8_t* v_codes;
+    void* v_meta;
+    const void* k;              // write: new rows [B][Hkv][L][d]
+    const void* v;
+    void* k_out;                // read: rows [B][Hkv][L][d]
+    void* v_out;
+    const void* q;              // attention: [B][Hkv * group][L][d]
+    void* o;
+    float* tau;                 // nullable [B][Hkv * group][L], x units
+    float alpha, gamma, cx;     // as in FwdArgs
+    int ntile;                  // query rows of a scores CTA / 8 (1, 2 or 4)
+    int chunk, nchunk;          // keys of a chunk, chunks of a call
+    float* chunk_max;           // workspace: [rows][nchunk], rows = B Hkv L group
+    int* chunk_n;               //            [rows][nchunk]
+    float* cand_x;              //            [rows][nchunk][chunk]
+    uint16_t* cand_j;           //            [rows][nchunk][chunk]
+};
+__host__ __device__ constexpr int kv4_chunk_keys(int ntile) { return ntile == 4 ? 256 : 512; }
+cudaError_t kv4_write(const Kv4Args& a, int d, bool bf16, cudaStream_t s);
+cudaError_t kv4_read(const Kv4Args& a, int d, bool bf16, cudaStream_t s);
+cudaError_t kv4_attn(const Kv4Args& a, int d, bool bf16, int gm, cudaStream_t s);
 
 // FP32 CUDA-core path: float32 inputs (scores by FFMA, no TF32 rounding).
 cudaError_t simt_fwd_f32(const FwdArgs& a, int d, int gm, cudaStream_t s);

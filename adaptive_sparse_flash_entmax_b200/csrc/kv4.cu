@@ -1,0 +1,782 @@
+// kv4.cu -- a paged key/value cache held in 4 bits, and alpha-entmax attention of the
+// newest tokens against it (layout and visibility: kv4_index.h).
+//
+//   kv4_write_kernel    new keys and values quantised as they are written;
+//   kv4_read_kernel     a stretch of every sequence as values again;
+//   kv4_scores_kernel   x = (alpha-1) q.k / sqrt(d) of a chunk of keys against the rows of
+//                       one key head, and the keys with x > (the chunk's maximum) - 1;
+//   kv4_solve_kernel    per query row: tau over all chunks' keys, then O = sum p_j v_j over
+//                       the support alone.
+// tau >= m - 1 (m the row maximum) and a chunk's maximum is at most m, so a key at or below
+// its chunk's maximum - 1 has p = 0: the scores never leave the chip but for the few that
+// can weigh, and value rows without a weight are never read.
+#include "kernels.h"
+
+#include <cuda_fp16.h>
+
+namespace ent {
+
+namespace {
+
+constexpr int kKvThreads = 256;
+constexpr unsigned kFull = 0xffffffffu;
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+__device__ __forceinline__ Kv4Seq seq_of(const Kv4Args& a, int b) {
+    return kv4_seq(a.g, a.start[b], a.new_lens ? a.new_lens[b] : a.g.L);
+}
+
+// 8 consecutive values of a row
+__device__ __forceinline__ void load8(const float* p, float* x) {
+    const float4 u = *reinterpret_cast<const float4*>(p), v = *reinterpret_cast<const float4*>(p + 4);
+    x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w; x[4] = v.x; x[5] = v.y; x[6] = v.z; x[7] = v.w;
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* x) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) { x[2 * i] = bf16_lo(w[i]); x[2 * i + 1] = bf16_hi(w[i]); }
+}
+__device__ __forceinline__ void store8(float* p, const float* x) {
+    *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+    *reinterpret_cast<float4*>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float* x) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// ------------------------------------------------------------------ write
+// Four threads per group of 32 dimensions, 8 each; blockIdx.y: 0 keys, 1 values.
+//     zero = bf16(min),  scale = bf16((max - zero) / 15),  code = rint((x - zero) / scale)
+// as they are in 64-bit arithmetic, so that the codes do not depend on who computes them:
+// the pair is computed in double by the group's threads, and an element's code in float
+// where its quotient is clear of a half-integer, in double where it is not (float's
+// quotient is within 2^-22 of it relative, at most 4e-6 for one up to 15.1; the few
+// elements nearer than 1e-4 to a tie, exact ties among them, take the division again).
+// A group with a NaN, an infinity, or a minimum that rounds to one is stored as (0, NaN):
+// it reads back as NaN.
+template <typename T, int D>
+__global__ void __launch_bounds__(kKvThreads) kv4_write_kernel(const Kv4Args a) {
+    constexpr int TPR = D / 8, G = D / kKvGroup;
+    const T* src = static_cast<const T*>(blockIdx.y ? a.v : a.k);
+    uint32_t* codes = reinterpret_cast<uint32_t*>(blockIdx.y ? a.v_codes : a.k_codes);
+    uint32_t* meta = reinterpret_cast<uint32_t*>(blockIdx.y ? a.v_meta : a.k_meta);
+    const long long item = (long long)blockIdx.x * kKvThreads + threadIdx.x;
+    const long long row = item / TPR;   // (b * Hkv + h) * L + l
+    const int t = (int)(item % TPR);
+    if (row >= (long long)a.g.B * a.Hkv * a.g.L) return;   // whole quads leave together
+    const int l = (int)(row % a.g.L);
+    const int bh = (int)(row / a.g.L), b = bh / a.Hkv, h = bh - b * a.Hkv;
+    const Kv4Seq s = seq_of(a, b);
+    if (s.bad && a.bad && l == 0 && t == 0) atomicOr(a.bad, s.bad);
+    if (l >= s.rows) return;
+    const int pos = s.start + l;
+    const int page = kv4_page(a.g, a.table + (size_t)b * a.g.max_pages, pos);
+    if (page < 0) {
+        if (a.bad && t == 0) atomicOr(a.bad, kKvBadPage);
+        return;
+    }
+    const unsigned quad = 0xfu << (threadIdx.x & 28);
+    float x[8];
+    load8(src + row * D + t * 8, x);
+    float lo = x[0], hi = x[0];
+    bool fine = isfinite(x[0]);
+#pragma unroll
+    for (int i = 1; i < 8; ++i) {
+        lo = fminf(lo, x[i]);
+        hi = fmaxf(hi, x[i]);
+        fine &= isfinite(x[i]);
+    }
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+        lo = fminf(lo, __shfl_xor_sync(quad, lo, o));
+        hi = fmaxf(hi, __shfl_xor_sync(quad, hi, o));
+        fine &= __shfl_xor_sync(quad, (int)fine, o) != 0;
+    }
+    const __nv_bfloat16 zb = __float2bfloat16_rn(lo);
+    const float z = __bfloat162float(zb);
+    fine &= isfinite(z);
+    const double range = (double)hi - (double)z;
+    const __nv_bfloat16 sb = __float2bfloat16_rn(fine && range > 0. ? (float)(range / 15.) : 0.f);
+    const float sc = __bfloat162float(sb);
+    uint32_t w = 0;
+    if (sc > 0.f) {
+        const float inv = 1.f / sc;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float qv = (x[i] - z) * inv;   // (an underflowing or overflowing inverse is caught below)
+            float r = rintf(qv);
+            if (!(fabsf(fabsf(qv - r) - 0.5f) > 1e-4f) || !(inv >= 1e-30f && inv <= 1e30f)) {
+                const double qd = ((double)x[i] - (double)z) / (double)sc;
+                r = (float)rint(qd);
+            }
+            w |= (uint32_t)fminf(fmaxf(r, 0.f), 15.f) << (4 * i);
+        }
+    }
+    const size_t at = kv4_row(a.g, a.Hkv, page, h, pos);
+    const int grp = t >> 2, c = t & 3;
+    codes[at * (D / 8) + c * G + grp] = w;
+    if (c == 0) {
+        const uint32_t zw = fine ? (uint32_t)__bfloat16_as_ushort(zb) : 0x7fffu;
+        meta[at * G + grp] = (uint32_t)__bfloat16_as_ushort(sb) | zw << 16;
+    }
+}
+
+// ------------------------------------------------------------------ read
+// A thread per word of codes: 8 values zero + scale * code (one fused multiply-add each:
+// exact but for the last rounding).  Rows past new_lens, and rows of a page outside the
+// pool, are zeros.
+template <typename T, int D>
+__global__ void __launch_bounds__(kKvThreads) kv4_read_kernel(const Kv4Args a) {
+    constexpr int TPR = D / 8, G = D / kKvGroup;
+    T* dst = static_cast<T*>(blockIdx.y ? a.v_out : a.k_out);
+    const uint32_t* codes = reinterpret_cast<const uint32_t*>(blockIdx.y ? a.v_codes : a.k_codes);
+    const uint32_t* meta = reinterpret_cast<const uint32_t*>(blockIdx.y ? a.v_meta : a.k_meta);
+    const long long item = (long long)blockIdx.x * kKvThreads + threadIdx.x;
+    const long long row = item / TPR;
+    const int t = (int)(item % TPR);
+    if (row >= (long long)a.g.B * a.Hkv * a.g.L) return;
+    const int l = (int)(row % a.g.L);
+    const int bh = (int)(row / a.g.L), b = bh / a.Hkv, h = bh - b * a.Hkv;
+    const Kv4Seq s = seq_of(a, b);
+    if (s.bad && a.bad && l == 0 && t == 0) atomicOr(a.bad, s.bad);
+    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    const int grp = t >> 2, c = t & 3;
+    if (l < s.rows) {
+        const int pos = s.start + l;
+        const int page = kv4_page(a.g, a.table + (size_t)b * a.g.max_pages, pos);
+        if (page >= 0) {
+            const size_t at = kv4_row(a.g, a.Hkv, page, h, pos);
+            const uint32_t w = codes[at * (D / 8) + c * G + grp];
+            const uint32_t m = meta[at * G + grp];
+            const float sc = bf16_lo(m), z = bf16_hi(m);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = fmaf(sc, (float)((w >> (4 * i)) & 15u), z);
+        } else if (a.bad && t == 0) {
+            atomicOr(a.bad, kKvBadPage);
+        }
+    }
+    store8(dst + row * D + t * 8, x);
+}
+
+// ------------------------------------------------------------------ scores
+// One CTA per (chunk of C keys, block of R = 8 NT rows, sequence and key head).  The rows
+// are the new tokens' queries of all heads that share the key head, row = l * group + head
+// of the group.  Keys are the M = 16 rows of an m16n8k16 product and the queries its 8
+// columns; the contraction index is permuted so that a lane's four A registers are its own
+// words of two keys, masked: a nibble at bits 0-3 of a half is code * 2^-24 (a subnormal,
+// which the product takes exactly), one at bits 4-7 is 16 times that, and the queries'
+// other operand carries the 1/16.  So 8 codes cost four ANDs and a shift, and the product
+// is exact in the codes.  The pair (scale, zero) of each group comes in afterwards:
+//     q.k = sum_groups scale * (codes . q) + zero * sum q.
+// The queries are fp16, scaled per row by a power of two so that the largest lies in
+// [2^14, 2^15): exact for bf16 values down to 2^-31 of the largest, below which the
+// rounding is 2^-39 of it; a float32 row is the sum of two such halves (22 bits).
+struct ChunkOut {
+    float* x;      // [rows][chunks][C] scores of the chunk's candidates, in key order
+    uint16_t* j;   // their key - the chunk's first key
+    float* m;      // [rows][chunks] maximum (NaN where a visible score is NaN or +inf)
+    int* n;        // [rows][chunks] candidates
+};
+
+__device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                          uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack_half(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// G consecutive 4-byte words (one load)
+template <int G>
+__device__ __forceinline__ void load_words(const uint32_t* p, uint32_t (&w)[G]) {
+    if constexpr (G == 4) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+        w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+    } else if constexpr (G == 2) {
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+        w[0] = v.x; w[1] = v.y;
+    } else {
+        w[0] = __ldg(p);
+    }
+}
+
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(kKvThreads) kv4_scores_kernel(const Kv4Args a) {
+    constexpr int G = D / kKvGroup, C = kv4_chunk_keys(NT), R = 8 * NT;
+    constexpr int kStride = C + 4;   // spreads a warp's 8 keys x 4 row pairs over the banks
+    constexpr int kTiles = C / kKvTile / (kKvThreads / 32);   // tiles of one warp
+    constexpr int U = kTiles < 4 ? kTiles : 4;                // of them in flight together
+    constexpr bool F32 = sizeof(T) == 4;
+    extern __shared__ float xs[];    // [R][kStride]
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int bk = blockIdx.z, b = bk / a.Hkv, hk = bk - b * a.Hkv;
+    const Kv4Seq s = seq_of(a, b);
+    if (s.bad && a.bad && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(a.bad, s.bad);
+    const int row0 = blockIdx.y * R, nrows = s.rows * a.group;   // real rows of this key head
+    int k0, k1;
+    kv4_chunk(a.g, s, C, blockIdx.x, &k0, &k1);
+    if (row0 >= nrows) return;
+    if (k0 >= k1) {
+        // a chunk of sinks that the sequence does not reach: empty, as the solver reads it
+        if (blockIdx.x < kv4_seq_chunks(a.g, s, C) && threadIdx.x < R && row0 + threadIdx.x < nrows) {
+            const size_t at = ((size_t)bk * a.g.L * a.group + row0 + threadIdx.x) * a.nchunk + blockIdx.x;
+            a.chunk_max[at] = -INFINITY;
+            a.chunk_n[at] = 0;
+        }
+        return;
+    }
+
+    // ---- queries: lane (n = lane / 4, c = lane % 4) holds dimensions 32 w + 8 c + i of row n
+    const int c = lane & 3;
+    uint32_t qf[NT][G][4], ql[F32 ? NT : 1][G][4];   // B operands; float32 rows: high and low parts
+    float qz[NT][G][2], mul[NT][2], mul2[NT][2];     // of this lane's columns 2c, 2c + 1
+    int pos[NT][2];                                  // their positions (-1: no row)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const int r = row0 + nt * 8 + (lane >> 2);
+        const bool real = r < nrows;
+        const int l = real ? r / a.group : 0, gi = real ? r - l * a.group : 0;
+        const T* q = static_cast<const T*>(a.q) + (((size_t)b * a.Hkv * a.group + hk * a.group + gi) * a.g.L + l) * D;
+        float x[G][8];
+        float top = 0.f;
+        bool fine = true;
+#pragma unroll
+        for (int w = 0; w < G; ++w) {
+            if (real) load8(q + 32 * w + 8 * c, x[w]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (!real) x[w][i] = 0.f;
+                fine &= isfinite(x[w][i]);
+                top = fmaxf(top, fabsf(x[w][i]));
+            }
+        }
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) {
+            top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+            fine &= __shfl_xor_sync(kFull, (int)fine, o) != 0;
+        }
+        int e = 0;
+        if (top > 0.f && fine) { frexpf(top, &e); e = 15 - e; }
+#pragma unroll
+        for (int w = 0; w < G; ++w) {
+            float sum = 0.f, hi[8], lo[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float y = ldexpf(x[w][i], e);
+                hi[i] = __half2float(__float2half_rn(y));
+                lo[i] = y - hi[i];
+                sum += y;
+            }
+            const float f = 0.0625f;
+            qf[nt][w][0] = pack_half(hi[0], hi[4]);
+            qf[nt][w][1] = pack_half(hi[1] * f, hi[5] * f);
+            qf[nt][w][2] = pack_half(hi[2], hi[6]);
+            qf[nt][w][3] = pack_half(hi[3] * f, hi[7] * f);
+            if constexpr (F32) {
+                ql[nt][w][0] = pack_half(lo[0], lo[4]);
+                ql[nt][w][1] = pack_half(lo[1] * f, lo[5] * f);
+                ql[nt][w][2] = pack_half(lo[2], lo[6]);
+                ql[nt][w][3] = pack_half(lo[3] * f, lo[7] * f);
+            }
+            sum += __shfl_xor_sync(kFull, sum, 1);
+            sum += __shfl_xor_sync(kFull, sum, 2);
+            sum *= 5.9604644775390625e-08f;   // 2^-24, the codes' unit
+            qz[nt][w][0] = __shfl_sync(kFull, sum, 8 * c);
+            qz[nt][w][1] = __shfl_sync(kFull, sum, 8 * c + 4);
+        }
+        // x = cx 2^(24 - e) s: in two factors, either of which is in range
+        const int e1 = (24 - e) / 2;
+        // a row with a NaN or an infinity has NaN scores
+        const float f1 = fine ? a.cx * ldexpf(1.f, e1) : nanf(""), f2 = ldexpf(1.f, 24 - e - e1);
+        const int p = real ? s.start + l : -1;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            mul[nt][k] = __shfl_sync(kFull, f1, 8 * c + 4 * k);
+            mul2[nt][k] = __shfl_sync(kFull, f2, 8 * c + 4 * k);
+            pos[nt][k] = __shfl_sync(kFull, p, 8 * c + 4 * k);
+        }
+    }
+    // every row of this block is real and sees every key of the chunk
+    const int first = s.start + row0 / a.group, last_r = row0 + R - 1;
+    const bool whole = last_r < nrows && k1 - k0 == C && k1 - 1 <= first &&
+                       (!a.g.window || k1 <= a.g.sinks || k0 > s.start + last_r / a.group - a.g.window);
+
+    // ---- keys, U tiles of a warp at a time
+    const int* table = a.table + (size_t)b * a.g.max_pages;
+    const uint32_t* codes = reinterpret_cast<const uint32_t*>(a.k_codes);
+    const uint32_t* meta = reinterpret_cast<const uint32_t*>(a.k_meta);
+    const int key = lane >> 2;   // the lane's keys of a tile: key and key + 8
+#pragma unroll
+    for (int t0 = 0; t0 < kTiles; t0 += U) {
+        uint32_t w[U][2][G], mt[U][2][G];
+        bool has[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int kb = k0 + ((t0 + u) * (kKvThreads / 32) + warp) * kKvTile;
+            int page = -1;
+            if (kb < k1) {
+                page = kv4_page(a.g, table, kb);
+                if (page < 0 && a.bad && lane == 0) atomicOr(a.bad, kKvBadPage);
+            }
+            has[u] = page >= 0;
+            if (has[u]) {
+                const size_t at = kv4_row(a.g, a.Hkv, page, hk, kb) + key;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    load_words<G>(codes + (at + 8 * h) * (D / 8) + c * G, w[u][h]);
+                    load_words<G>(meta + (at + 8 * h) * G, mt[u][h]);
+                }
+            } else {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int i = 0; i < G; ++i) { w[u][h][i] = 0u; mt[u][h][i] = 0u; }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int kt = ((t0 + u) * (kKvThreads / 32) + warp) * kKvTile;
+            float acc[NT][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) acc[nt][k] = 0.f;
+#pragma unroll
+            for (int i = 0; i < G; ++i) {
+                uint32_t w0 = w[u][0][i], w1 = w[u][1][i];
+                uint32_t av[8];
+                av[0] = w0 & 0x000f000fu; av[1] = w1 & 0x000f000fu;
+                av[2] = w0 & 0x00f000f0u; av[3] = w1 & 0x00f000f0u;
+                w0 >>= 8; w1 >>= 8;
+                av[4] = w0 & 0x000f000fu; av[5] = w1 & 0x000f000fu;
+                av[6] = w0 & 0x00f000f0u; av[7] = w1 & 0x00f000f0u;
+                const float s0 = bf16_lo(mt[u][0][i]), z0 = bf16_hi(mt[u][0][i]);
+                const float s1 = bf16_lo(mt[u][1][i]), z1 = bf16_hi(mt[u][1][i]);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float d[4] = {0.f, 0.f, 0.f, 0.f};
+                    mma_16816(d, av[0], av[1], av[2], av[3], qf[nt][i][0], qf[nt][i][1]);
+                    mma_16816(d, av[4], av[5], av[6], av[7], qf[nt][i][2], qf[nt][i][3]);
+                    if constexpr (F32) {
+                        mma_16816(d, av[0], av[1], av[2], av[3], ql[nt][i][0], ql[nt][i][1]);
+                        mma_16816(d, av[4], av[5], av[6], av[7], ql[nt][i][2], ql[nt][i][3]);
+                    }
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        acc[nt][k] = fmaf(s0, d[k], fmaf(z0, qz[nt][i][k], acc[nt][k]));
+                        acc[nt][2 + k] = fmaf(s1, d[2 + k], fmaf(z1, qz[nt][i][k], acc[nt][2 + k]));
+                    }
+                }
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const int j = k0 + kt + key + 8 * h;
+                        float x = acc[nt][2 * h + k] * mul[nt][k] * mul2[nt][k];
+                        if (!whole || !has[u])
+                            x = (has[u] && j < k1 && kv4_sees(a.g, pos[nt][k], j)) ? x : -INFINITY;
+                        xs[(nt * 8 + 2 * c + k) * kStride + kt + key + 8 * h] = x;
+                    }
+        }
+    }
+    __syncthreads();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    // ---- a warp per row: maximum, then the candidates in key order
+    const ChunkOut out{a.cand_x, a.cand_j, a.chunk_max, a.chunk_n};
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const int r = nt * 8 + warp;
+        if (row0 + r >= nrows) break;
+        float v[C / 32];
+        float m = -INFINITY;
+        bool nan = false;
+#pragma unroll
+        for (int e = 0; e < C / 32; ++e) {
+            v[e] = xs[r * kStride + e * 32 + lane];
+            nan |= !(v[e] < INFINITY);
+            m = fmaxf(m, v[e]);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+        nan = __any_sync(kFull, nan);
+        const size_t at = ((size_t)bk * a.g.L * a.group + row0 + r) * a.nchunk + blockIdx.x;
+    // the maximum itself is always kept: at |m| >= 2^24 it equals m - 1
+        const float lim = m - 1.f;
+        float* ox = out.x + at * C;
+        uint16_t* oj = out.j + at * C;
+        int n = 0;
+        if (!nan) {
+#pragma unroll
+            for (int e = 0; e < C / 32; ++e) {
+                const bool take = v[e] > lim || (v[e] == m && m > -INFINITY);
+                const unsigned mask = __ballot_sync(kFull, take);
+                if (take) {
+                    const int i = n + __popc(mask & ((1u << lane) - 1u));
+                    ox[i] = v[e];
+                    oj[i] = (uint16_t)(e * 32 + lane);
+                }
+                n += __popc(mask);
+            }
+        }
+        if (lane == 0) {
+            out.m[at] = nan ? nanf("") : m;
+            out.n[at] = n;
+        }
+    }
+}
+
+// ------------------------------------------------------------------ solve and P.V
+// One CTA per query row.  The candidates above m - 1 (m the maximum over the chunks) are
+// gathered in key order into shared memory (kCap of them; a row with more goes over the
+// chunks' lists again in every pass), tau - m is found by Halley-bisection from the bracket
+// [-1, -n^(1-alpha)] (n the candidates' count: f <= 0 there since at most n keys weigh),
+// and O accumulates over the support, D/8 lanes per value row.  Scores are held relative
+// to m, so tau keeps its precision for scores of any size.  Every sum has a fixed order:
+// the result does not change from run to run.
+constexpr int kSolveThreads = 128;
+constexpr int kSolveWarps = kSolveThreads / 32;
+constexpr int kCap = 2048;
+constexpr float kKvFtol = 2e-7f, kKvStol = 6e-8f;   // to the rounding of the sums
+
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(kFull, x, o);
+    return x;
+}
+
+// Exclusive prefix over the CTA's warps of one count each; total in *all.  Two barriers.
+__device__ __forceinline__ int warps_before(int n, int* box, int* all) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    __syncthreads();
+    if (lane == 0) box[warp] = n;
+    __syncthreads();
+    int before = 0, sum = 0;
+#pragma unroll
+    for (int w = 0; w < kSolveWarps; ++w) {
+        if (w < warp) before += box[w];
+        sum += box[w];
+    }
+    *all = sum;
+    return before;
+}
+
+template <typename T, int D, int GM>
+__global__ void __launch_bounds__(kSolveThreads) kv4_solve_kernel(const Kv4Args a) {
+    constexpr int G = D / kKvGroup, LPK = D / 8, KPW = 32 / LPK;
+    __shared__ float ys[kCap];          // x - m of the candidates, then their weights
+    __shared__ int js[kCap];            // their keys
+    __shared__ float red[3][kSolveWarps];
+    __shared__ int box[kSolveWarps];
+    __shared__ float bc[2];
+    __shared__ float part[kSolveWarps][D];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = a.g.L * a.group;    // rows of one key head
+    const int bk = blockIdx.x / per, r = blockIdx.x - bk * per;
+    const int b = bk / a.Hkv, hk = bk - b * a.Hkv;
+    const int l = r / a.group, gi = r - l * a.group;
+    const Kv4Seq s = seq_of(a, b);
+    const size_t orow = ((size_t)b * a.Hkv * a.group + hk * a.group + gi) * a.g.L + l;
+    T* o = static_cast<T*>(a.o) + orow * D;
+    const int C = a.chunk;
+    const int nch = l < s.rows ? kv4_seq_chunks(a.g, s, C) : 0;
+    const size_t at = ((size_t)bk * per + r) * a.nchunk;
+    const float* cm = a.chunk_max + at;
+    const int* cn = a.chunk_n + at;
+    const float* cx = a.cand_x + at * C;
+    const uint16_t* cj = a.cand_j + at * C;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    // ---- row maximum
+    float m = -INFINITY;
+    bool nan = false;
+    for (int i = tid; i < nch; i += kSolveThreads) {
+        const float x = cm[i];
+        nan |= x != x;
+        m = fmaxf(m, x);
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, d));
+    if (lane == 0) red[0][warp] = m;
+    nan = __syncthreads_or(nan);
+#pragma unroll
+    for (int w = 0; w < kSolveWarps; ++w) m = fmaxf(m, red[0][w]);
+    if (nan || m == -INFINITY) {   // no key is seen: zeros
+        const float v = nan ? nanf("") : 0.f;
+        for (int i = tid; i < D; i += kSolveThreads) store_f(o, i, v);
+        if (tid == 0 && a.tau) a.tau[orow] = v;
+        return;
+    }
+
+    // ---- candidates: each warp takes a run of chunks, counts, then places
+    const int c0 = (int)((long long)nch * warp / kSolveWarps), c1 = (int)((long long)nch * (warp + 1) / kSolveWarps);
+    int mine = 0;
+    for (int i = c0; i < c1; ++i) {
+        if (!(cm[i] - m > -1.f)) continue;
+        const int n = cn[i];
+        for (int e = lane; e < n; e += 32) mine += cx[(size_t)i * C + e] - m > -1.f;
+    }
+    mine = __reduce_add_sync(kFull, mine);
+    int total;
+    int put = warps_before(mine, box, &total);
+    const bool fits = total <= kCap;
+    if (fits) {
+        for (int i = c0; i < c1; ++i) {
+            if (!(cm[i] - m > -1.f)) continue;
+            const int n = cn[i];
+            int k0, k1;
+            kv4_chunk(a.g, s, C, i, &k0, &k1);
+            for (int e0 = 0; e0 < n; e0 += 32) {
+                const int e = e0 + lane;
+                const float y = e < n ? cx[(size_t)i * C + e] - m : -2.f;
+                const unsigned mask = __ballot_sync(kFull, y > -1.f);
+                if (y > -1.f) {
+                    const int p = put + __popc(mask & ((1u << lane) - 1u));
+                    ys[p] = y;
+                    js[p] = k0 + cj[(size_t)i * C + e];
+                }
+                put += __popc(mask);
+            }
+        }
+    }
+    __syncthreads();
+
+    // ---- tau - m
+    const float gamma = a.gamma;
+    RowSolver sv;
+    sv.done = 0;
+    sv.iters = 0;
+    sv.lo = -1.f;
+    sv.hi = fmaxf(-1.f, -exp2f((1.f - a.alpha) * __log2f((float)total)) + 1e-6f);
+    sv.tau = 0.5f * (sv.lo + sv.hi);
+    for (int pass = 1;; ++pass) {
+        float F0 = 0.f, F1 = 0.f, F2 = 0.f;
+        auto add = [&](float y) {
+            float t0, t1, t2;
+            entmax_terms_bf<GM>(y - sv.tau, gamma, t0, t1, t2);
+            F0 += t0; F1 += t1; F2 += t2;
+        };
+        if (fits) {
+            for (int i = tid; i < total; i += kSolveThreads) add(ys[i]);
+        } else {
+            for (int i = c0; i < c1; ++i) {
+                if (!(cm[i] - m > -1.f)) continue;
+                const int n = cn[i];
+                for (int e = lane; e < n; e += 32) add(cx[(size_t)i * C + e] - m);
+            }
+        }
+        F0 = warp_sum(F0); F1 = warp_sum(F1); F2 = warp_sum(F2);
+        if (lane == 0) { red[0][warp] = F0; red[1][warp] = F1; red[2][warp] = F2; }
+        __syncthreads();
+        if (tid == 0) {
+            F0 = F1 = F2 = 0.f;
+            for (int w = 0; w < kSolveWarps; ++w) { F0 += red[0][w]; F1 += red[1][w]; F2 += red[2][w]; }
+            solver_update(sv, F0, F1, F2, gamma, gamma == 1.f, pass, kKvFtol, kKvStol);
+            bc[0] = sv.tau;
+            bc[1] = sv.done ? 1.f : 0.f;
+        }
+        __syncthreads();
+        sv.tau = bc[0];
+        if (bc[1] != 0.f) break;
+    }
+    if (tid == 0 && a.tau) a.tau[orow] = sv.tau + m;
+
+    // ---- O over the support
+    const int slot = lane / LPK, t = lane - slot * LPK;   // key slot of the warp, word of the row
+    const int grp = t % G;
+    const int* table = a.table + (size_t)b * a.g.max_pages;
+    const uint32_t* codes = reinterpret_cast<const uint32_t*>(a.v_codes);
+    const uint32_t* meta = reinterpret_cast<const uint32_t*>(a.v_meta);
+    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, accz = 0.f;
+    auto fetch = [&](int j, uint32_t& w, uint32_t& mt) {
+        const int page = kv4_page(a.g, table, j);
+        w = mt = 0u;
+        if (page >= 0) {
+            const size_t row = kv4_row(a.g, a.Hkv, page, hk, j);
+            w = __ldg(codes + row * (D / 8) + t);
+            mt = __ldg(meta + row * G + grp);
+        }
+    };
+    auto weigh = [&](float p, uint32_t w, uint32_t mt) {
+        const float ps = p * bf16_lo(mt);
+        accz = fmaf(p, bf16_hi(mt), accz);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] = fmaf(ps, (float)((w >> (4 * i)) & 15u), acc[i]);
+    };
+    if (fits) {
+        // the support in key order, over the same arrays: each warp compacts its run, then
+        // the runs are closed up
+        const int e0 = (int)((long long)total * warp / kSolveWarps), e1 = (int)((long long)total * (warp + 1) / kSolveWarps);
+        int n = 0;
+        for (int base = e0; base < e1; base += 32) {
+            const int e = base + lane;
+            const float p = e < e1 ? entmax_p<GM>(ys[e] - sv.tau, gamma) : 0.f;
+            const int j = e < e1 ? js[e] : 0;
+            const unsigned mask = __ballot_sync(kFull, p > 0.f);
+            __syncwarp();
+            if (p > 0.f) {
+                const int q = e0 + n + __popc(mask & ((1u << lane) - 1u));
+                ys[q] = p;
+                js[q] = j;
+            }
+            n += __popc(mask);
+            __syncwarp();
+        }
+        int sup;
+        warps_before(n, box, &sup);
+        __syncthreads();
+        // entry i of the support: in the run of the warp whose counts it falls into
+        int ends[kSolveWarps];
+#pragma unroll
+        for (int w = 0, sum = 0; w < kSolveWarps; ++w) { sum += box[w]; ends[w] = sum; }
+        auto where = [&](int i) {
+            int w = 0, before = 0;
+#pragma unroll
+            for (int k = 0; k + 1 < kSolveWarps; ++k)
+                if (i >= ends[k]) { w = k + 1; before = ends[k]; }
+            return (int)((long long)total * w / kSolveWarps) + i - before;
+        };
+        constexpr int U = 4, STEP = kSolveWarps * KPW;
+        for (int i0 = warp * KPW + slot; i0 < sup; i0 += U * STEP) {
+            float p[U];
+            uint32_t w[U], mt[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int i = i0 + u * STEP;
+                p[u] = 0.f;
+                w[u] = mt[u] = 0u;
+                if (i < sup) {
+                    const int q = where(i);
+                    p[u] = ys[q];
+                    fetch(js[q], w[u], mt[u]);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) weigh(p[u], w[u], mt[u]);
+        }
+    } else {
+        for (int i = c0; i < c1; ++i) {
+            if (!(cm[i] - m > sv.tau)) continue;
+            const int n = cn[i];
+            int k0, k1;
+            kv4_chunk(a.g, s, C, i, &k0, &k1);
+            for (int e = slot; e < n; e += KPW) {
+                const float p = entmax_p<GM>(cx[(size_t)i * C + e] - m - sv.tau, gamma);
+                if (!(p > 0.f)) continue;
+                uint32_t w, mt;
+                fetch(k0 + cj[(size_t)i * C + e], w, mt);
+                weigh(p, w, mt);
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        acc[i] += accz;
+#pragma unroll
+        for (int d = LPK; d < 32; d <<= 1) acc[i] += __shfl_xor_sync(kFull, acc[i], d);
+    }
+    if (slot == 0) {
+        // word t = c G + w holds dimensions 32 w + 8 c ..
+#pragma unroll
+        for (int i = 0; i < 8; ++i) part[warp][32 * (t % G) + 8 * (t / G) + i] = acc[i];
+    }
+    __syncthreads();
+    for (int i = tid; i < D; i += kSolveThreads) {
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < kSolveWarps; ++w) v += part[w][i];
+        store_f(o, i, v);
+    }
+}
+
+// ------------------------------------------------------------------ launches
+template <typename T, int D>
+cudaError_t write_or_read(const Kv4Args& a, bool write, cudaStream_t s) {
+    const long long items = (long long)a.g.B * a.Hkv * a.g.L * (D / 8);
+    const dim3 grid((unsigned)((items + kKvThreads - 1) / kKvThreads), 2);
+    if (write) kv4_write_kernel<T, D><<<grid, kKvThreads, 0, s>>>(a);
+    else kv4_read_kernel<T, D><<<grid, kKvThreads, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+template <typename T, int D, int NT>
+cudaError_t launch_scores(const Kv4Args& a, cudaStream_t s) {
+    const int rows = a.g.L * a.group;
+    const size_t sm = (size_t)8 * NT * (kv4_chunk_keys(NT) + 4) * sizeof(float);
+    auto kern = kv4_scores_kernel<T, D, NT>;
+    if (sm > 48 * 1024) {
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
+        if (e != cudaSuccess) return e;
+    }
+    kern<<<dim3(a.nchunk, (rows + 8 * NT - 1) / (8 * NT), a.g.B * a.Hkv), kKvThreads, sm, s>>>(a);
+    return cudaGetLastError();
+}
+
+template <typename T, int D>
+cudaError_t attn(const Kv4Args& a, int gm, cudaStream_t s) {
+    cudaError_t e = cudaSuccess;
+    if (a.nchunk > 0) switch (a.ntile) {   // (a call that covers no token: zeros only)
+        case 1: e = launch_scores<T, D, 1>(a, s); break;
+        case 2: e = launch_scores<T, D, 2>(a, s); break;
+        default: e = launch_scores<T, D, 4>(a, s); break;
+    }
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(a.g.B * a.Hkv * a.g.L * a.group));
+    cfg.blockDim = dim3(kSolveThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    switch (gm) {
+        case 1: return cudaLaunchKernelEx(&cfg, kv4_solve_kernel<T, D, 1>, a);
+        case 2: return cudaLaunchKernelEx(&cfg, kv4_solve_kernel<T, D, 2>, a);
+        case 3: return cudaLaunchKernelEx(&cfg, kv4_solve_kernel<T, D, 3>, a);
+        case 4: return cudaLaunchKernelEx(&cfg, kv4_solve_kernel<T, D, 4>, a);
+        default: return cudaLaunchKernelEx(&cfg, kv4_solve_kernel<T, D, 0>, a);
+    }
+}
+
+}  // namespace
+
+cudaError_t kv4_write(const Kv4Args& a, int d, bool bf16, cudaStream_t s) {
+    if (bf16) return d == 128 ? write_or_read<__nv_bfloat16, 128>(a, true, s)
+                   : d == 64 ? write_or_read<__nv_bfloat16, 64>(a, true, s)
+                             : write_or_read<__nv_bfloat16, 32>(a, true, s);
+    return d == 128 ? write_or_read<float, 128>(a, true, s)
+         : d == 64 ? write_or_read<float, 64>(a, true, s) : write_or_read<float, 32>(a, true, s);
+}
+
+cudaError_t kv4_read(const Kv4Args& a, int d, bool bf16, cudaStream_t s) {
+    if (bf16) return d == 128 ? write_or_read<__nv_bfloat16, 128>(a, false, s)
+                   : d == 64 ? write_or_read<__nv_bfloat16, 64>(a, false, s)
+                             : write_or_read<__nv_bfloat16, 32>(a, false, s);
+    return d == 128 ? write_or_read<float, 128>(a, false, s)
+         : d == 64 ? write_or_read<float, 64>(a, false, s) : write_or_read<float, 32>(a, false, s);
+}
+
+cudaError_t kv4_attn(const Kv4Args& a, int d, bool bf16, int gm, cudaStream_t s) {
+    if (bf16) return d == 128 ? attn<__nv_bfloat16, 128>(a, gm, s)
+                   : d == 64 ? attn<__nv_bfloat16, 64>(a, gm, s) : attn<__nv_bfloat16, 32>(a, gm, s);
+    return d == 128 ? attn<float, 128>(a, gm, s) : d == 64 ? attn<float, 64>(a, gm, s) : attn<float, 32>(a, gm, s);
+}
+
+}  // namespace ent

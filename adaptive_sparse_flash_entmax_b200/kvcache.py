@@ -1,0 +1,193 @@
+"""A paged key/value cache held in 4 bits, and alpha-entmax attention of the newest tokens against it
+(wrappers of the ``ent_attn_kv4_*`` calls of include/entattn.h, which states the format).
+
+A step of a decoder layer, B sequences with up to L new tokens each::
+
+    cache = kv4_alloc(pages, heads, page, d, device)              # once
+    kv4_write(cache, k, v, block_table, start, new_lens)          # k, v [B, Hkv, L, d]
+    o = entmax_attn_kv4(q, cache, block_table, start, alpha, new_lens=new_lens)   # q [B, Hq, L, d]
+
+``block_table`` int32 [B, max_pages] names the pages of each sequence in order, ``start`` int32 [B] the
+position of row 0 (the tokens cached before), ``new_lens`` int32 [B] the rows that are real (None: all L).
+"""
+from __future__ import annotations
+
+from typing import NamedTuple
+
+import torch
+
+from . import capi
+from .attention import _DTYPES, _raise, _stream_handle
+
+_GROUP = 32
+
+
+class KV4Cache(NamedTuple):
+    """The pool's arrays: codes uint8 [pages, heads, page, d/2], meta bfloat16 [pages, heads, page,
+    d/32, 2].  Every function here takes a plain tuple of the four as well."""
+    k_codes: torch.Tensor
+    k_meta: torch.Tensor
+    v_codes: torch.Tensor
+    v_meta: torch.Tensor
+
+
+def kv4_alloc(pages: int, heads: int, page: int, d: int, device="cuda") -> KV4Cache:
+    """A pool of ``pages`` pages of ``page`` tokens (a power of two, at least 16), all zeros."""
+    if d not in (32, 64, 128):
+        raise ValueError(f"head dim {d} not supported (32, 64 or 128)")
+    if page < 16 or page & (page - 1):
+        raise ValueError(f"page must be a power of two of at least 16, not {page}")
+    shape = (pages, heads, page)
+    return KV4Cache(*(torch.zeros(shape + tail, dtype=t, device=device)
+                      for _ in "kv" for tail, t in (((d // 2,), torch.uint8),
+                                                    ((d // _GROUP, 2), torch.bfloat16))))
+
+
+def _check_cache(cache, device):
+    """(pages, heads, page, d) of the pool."""
+    kc, km, vc, vm = cache
+    if kc.dim() != 4:
+        raise ValueError(f"expected codes [pages, heads, page, d/2], got shape {tuple(kc.shape)}")
+    pages, heads, page, half = kc.shape
+    meta = (pages, heads, page, half // 16, 2)
+    if (vc.shape != kc.shape or km.shape != meta or vm.shape != meta or kc.dtype != torch.uint8
+            or vc.dtype != torch.uint8 or km.dtype != torch.bfloat16 or vm.dtype != torch.bfloat16):
+        raise ValueError("the cache must be codes uint8 [pages, heads, page, d/2] and meta bfloat16 "
+                         "[pages, heads, page, d/32, 2], keys and values alike")
+    if not (kc.device == km.device == vc.device == vm.device == device):
+        raise ValueError("the cache must be on the device of the other tensors")
+    if not (kc.is_contiguous() and km.is_contiguous() and vc.is_contiguous() and vm.is_contiguous()):
+        raise ValueError("the cache's arrays must be contiguous")
+    return pages, heads, page, 2 * half
+
+
+def _check_seqs(block_table, start, new_lens, bad, B, device):
+    """Device pointers (table, start, new_lens or None, bad or None) and the table's columns."""
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError(f"expected block_table [{B}, max_pages], got shape {tuple(block_table.shape)}")
+    for t, shape in ((block_table, block_table.shape), (start, (B,)), (new_lens, (B,)), (bad, (1,))):
+        if t is None:
+            continue
+        if t.dtype != torch.int32 or t.shape != shape or t.device != device or not t.is_contiguous():
+            raise ValueError("block_table, start, new_lens and bad must be contiguous int32 tensors of "
+                             "shapes [B, max_pages], [B], [B] and [1] on the device of the others")
+    return (block_table.data_ptr(), start.data_ptr(), new_lens.data_ptr() if new_lens is not None else None,
+            bad.data_ptr() if bad is not None else None, block_table.shape[1])
+
+
+def _check_rows4(*ts):
+    t0 = ts[0]
+    if t0.dim() != 4:
+        raise ValueError(f"expected [B, H, L, d] tensors, got shape {tuple(t0.shape)}")
+    if t0.dtype not in _DTYPES:
+        raise ValueError(f"dtype {t0.dtype} not supported (float32 or bfloat16)")
+    for t in ts:
+        if t.shape != t0.shape or t.dtype != t0.dtype or t.device != t0.device:
+            raise ValueError("tensors must share shape, dtype and device")
+    for t in ts:
+        if not t.is_cuda or not t.is_contiguous():
+            raise ValueError("tensors must be contiguous CUDA tensors")
+
+
+def _call(fn, device, *args):
+    """fn(*args, stream) with the tensors' device current."""
+    if device.index == torch.cuda.current_device():
+        st = fn(*args, _stream_handle(device))
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, _stream_handle(device))
+    _raise(st, fn.__name__)
+
+
+def kv4_write(cache, k, v, block_table, start, new_lens=None, *, bad=None) -> None:
+    """Quantise k, v [B, Hkv, L, d] into the cache at positions start .. start + new_lens - 1.
+
+    ``bad`` (int32 [1], zeroed by the caller) gets bit 0 set where a page number lies outside the pool,
+    bit 1 where a start or length lies outside the table; the rows concerned are not written.  Pages
+    being written must belong to one sequence."""
+    _check_rows4(k, v)
+    B, H, L, d = k.shape
+    pages, heads, page, dc = _check_cache(cache, k.device)
+    if (heads, dc) != (H, d):
+        raise ValueError(f"the cache holds {heads} heads of {dc}, not {H} of {d}")
+    table, st, nl, bp, max_pages = _check_seqs(block_table, start, new_lens, bad, B, k.device)
+    _call(capi.ent_attn_kv4_write, k.device, k.data_ptr(), v.data_ptr(), B, H, L, d, _DTYPES[k.dtype],
+          table, max_pages, st, nl, *(t.data_ptr() for t in cache), pages, page, bp)
+
+
+def kv4_read(cache, block_table, start, n: int, new_lens=None, *, dtype=torch.bfloat16, out=None, bad=None):
+    """The cached values of positions start .. start + n - 1 (``new_lens``: of its first rows only, the
+    rest zeros): (k, v) [B, Hkv, n, d] in ``dtype`` (float32 or bfloat16), or in ``out``."""
+    device = block_table.device
+    pages, heads, page, d = _check_cache(cache, device)
+    B = block_table.shape[0]
+    if out is None:
+        if dtype not in _DTYPES:
+            raise ValueError(f"dtype {dtype} not supported (float32 or bfloat16)")
+        if n < 0:
+            raise ValueError(f"negative n={n}")
+        k = torch.empty((B, heads, n, d), dtype=dtype, device=device)
+        v = torch.empty_like(k)
+    else:
+        k, v = out
+        if k.shape != (B, heads, n, d):
+            raise ValueError(f"out must be of shape {(B, heads, n, d)}, not {tuple(k.shape)}")
+    _check_rows4(k, v)
+    table, st, nl, bp, max_pages = _check_seqs(block_table, start, new_lens, bad, B, device)
+    _call(capi.ent_attn_kv4_read, device, *(t.data_ptr() for t in cache), pages, page, table, max_pages,
+          st, nl, B, heads, n, d, _DTYPES[k.dtype], k.data_ptr(), v.data_ptr(), bp)
+    return k, v
+
+
+def kv4_workspace(q, cache, block_table, *, window: int | None = None, sinks: int = 0,
+                  max_len: int | None = None) -> torch.Tensor:
+    """A workspace for ``entmax_attn_kv4`` of these arguments; it serves one call at a time."""
+    B, Hq, L, d = q.shape
+    cap = block_table.shape[1] * cache[0].shape[2]
+    n = capi.ent_attn_kv4_workspace_size(B, Hq, cache[0].shape[1], L, d, _DTYPES[q.dtype],
+                                         cap if max_len is None else max_len, window or 0, sinks)
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=q.device)
+
+
+def entmax_attn_kv4(q, cache, block_table, start, alpha: float = 1.5, *, new_lens=None,
+                    window: int | None = None, sinks: int = 0, max_len: int | None = None, out=None,
+                    tau=None, ws: torch.Tensor | None = None, bad=None):
+    """O [B, Hq, L, d] of the newest tokens' queries against the cache (their keys are in it already).
+
+    Row l of sequence b, at position i = start[b] + l, sees key j when j <= i and, with a ``window``,
+    i - j < window or j < sinks; rows from new_lens[b] on give zeros.  Query head h reads key head
+    h // (Hq // Hkv).  ``max_len`` bounds start + new_lens (default: what the table covers) and sizes
+    the workspace; ``tau`` (float32 [B, Hq, L]) also takes the rows' thresholds; ``bad`` as in
+    ``kv4_write``.  No gradient."""
+    _check_rows4(q)
+    B, Hq, L, d = q.shape
+    device = q.device
+    pages, heads, page, dc = _check_cache(cache, device)
+    if dc != d or Hq % heads:
+        raise ValueError(f"the cache holds {heads} heads of {dc}; q has {Hq} of {d}")
+    if window is None:
+        if sinks:
+            raise ValueError("sinks need a window")
+        window = 0
+    elif window < 1 or sinks < 0:
+        raise ValueError(f"window must be at least 1 and sinks at least 0, not {window} and {sinks}")
+    table, st, nl, bp, max_pages = _check_seqs(block_table, start, new_lens, bad, B, device)
+    if max_len is None:
+        max_len = max_pages * page
+    dt = _DTYPES[q.dtype]
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _check_rows4(q, out)
+    if tau is not None and (tau.dtype != torch.float32 or tau.shape != (B, Hq, L) or tau.device != device
+                            or not tau.is_contiguous()):
+        raise ValueError("tau must be a contiguous float32 tensor [B, Hq, L] on the device of q")
+    need = capi.ent_attn_kv4_workspace_size(B, Hq, heads, L, d, dt, max_len, window, sinks)
+    if ws is None or ws.numel() < need:
+        ws = torch.empty(max(need, 256), dtype=torch.uint8, device=device)
+    elif ws.dtype != torch.uint8 or ws.device != device or not ws.is_contiguous():
+        raise ValueError("ws must be a contiguous uint8 tensor on the device of q")
+    _call(capi.ent_attn_kv4_fwd, device, q.data_ptr(), B, Hq, heads, L, d, dt, alpha, window, sinks,
+          *(t.data_ptr() for t in cache), pages, page, table, max_pages, st, nl, max_len, out.data_ptr(),
+          tau.data_ptr() if tau is not None else None, bp, ws.data_ptr(), ws.numel())
+    return out

@@ -317,6 +317,82 @@ ent_status ent_entmax_rows_fwd(const void *z, int rows, int n, int dtype, float 
 ent_status ent_entmax_rows_bwd(const void *z, const float *tau, const void *dp, int rows, int n,
                                int dtype, float alpha, void *dz, void *stream);
 
+/*
+ * A paged key/value cache held in 4 bits, and alpha-entmax attention of the newest
+ * tokens against it (serving: no gradient).  The pages of the method describe training
+ * attention only; the cache and its format are this library's own.
+ *
+ * The pool: four device arrays owned by the caller, 16-byte aligned,
+ *   k_codes, v_codes  uint8 [pages][Hkv][page][d/2],
+ *   k_meta, v_meta    bfloat16 [pages][Hkv][page][d/32][2]: (scale, zero) of each 32
+ *                     consecutive dimensions,
+ * page a power of two >= 16 (tokens).  A group of 32 values x is held as
+ *   zero = bf16(min x), scale = bf16((max x - zero) / 15) (0 where max x <= zero),
+ *   code = (x - zero) / scale rounded to the nearest integer (ties to even), clamped to
+ *   [0, 15] (0 where scale = 0),
+ * computed as in 64-bit arithmetic, and stands for zero + scale * code: within
+ * scale/2 of x, plus the rounding of zero.  A group that holds a NaN or an infinity (or
+ * whose minimum rounds to one) is held as (0, NaN) and stands for NaN.  The 4-byte word
+ * c * (d/32) + w of a token's codes (c = 0..3) holds dimension 32 w + 8 c + i in bits
+ * 4i .. 4i+3.
+ *
+ * Sequences: block_table int32 [B][max_pages] names the page that holds tokens
+ * [p * page, (p + 1) * page) of a sequence in its entry p; start int32 [B] is the
+ * position of row 0 of the call's L rows, and new_lens int32 [B] (nullable: L for all)
+ * how many of the L rows are real; rows from new_lens on are padding.  All three are
+ * device arrays, read by the kernels.  What the host cannot check is checked there:
+ *   a page number outside [0, pages)   the row is not written / reads as zeros / its
+ *                                      keys are not seen;
+ *   start or new_lens negative or      the rows outside the cover (max_pages * page
+ *   beyond the cover                   tokens, max_len for the attention) are treated
+ *                                      as padding (a negative one: all rows);
+ * and bad (nullable, one device int32, zeroed by the caller) gets bit 0 (1) for the
+ * former and bit 1 (2) for the latter or'ed in.  No call reads or writes outside the
+ * arrays whatever the three hold.
+ *
+ * ent_attn_kv4_write quantises k, v [B][Hkv][L][d] (dtype ENT_F32 or ENT_BF16) into the
+ * pool at positions start .. start + new_lens - 1.  Pages being written must belong to
+ * one sequence: where two rows of a call go to the same place, that place holds parts of
+ * either afterwards.
+ *
+ * ent_attn_kv4_read writes the values of positions start .. start + new_lens - 1 to
+ * k, v [B][Hkv][L][d] in dtype; padding rows are zeros.
+ *
+ * ent_attn_kv4_fwd: for the query rows q [B][Hq][L][d] (Hq a multiple of Hkv; query head
+ * h reads key head h / (Hq / Hkv)) of the L newest tokens, whose keys are already in the
+ * cache, O [B][Hq][L][d] with
+ *   row l at position i = start + l sees key j iff j <= i and (window == 0 or
+ *   i - j < window or j < sinks),
+ *   x_j = (alpha-1) q.k_j / sqrt(d), p = (x - tau)_+^(1/(alpha-1)), sum p = 1, o = sum p_j v_j
+ * over the cached values, sums in float.  Value rows whose key has no weight are not read.  Padding rows and rows that
+ * see no key (their pages missing) give zeros (tau 0); rows with a NaN or an infinite
+ * score give NaN.  tau (nullable) float [B][Hq][L], in units of x, absolute.  max_len (at
+ * most max_pages * page) bounds start + new_lens and sizes the workspace,
+ * ent_attn_kv4_workspace_size (0 for sizes the call refuses); a workspace belongs to one
+ * call at a time.  The result does not depend on what else runs, and is the same from
+ * call to call.
+ *
+ * Limits: d in {32, 64, 128}, B * Hkv <= 65535, max_pages * page <= 2^30, 1 < alpha <= 2, window, sinks >= 0
+ * (sinks need a window).  B, L = 0 is a no-op.  Asynchronous on `stream`, no allocation.
+ */
+ent_status ent_attn_kv4_write(const void *k, const void *v, int B, int Hkv, int L, int d, int dtype,
+                              const int32_t *block_table, int max_pages, const int32_t *start,
+                              const int32_t *new_lens, void *k_codes, void *k_meta, void *v_codes,
+                              void *v_meta, int pages, int page, int32_t *bad, void *stream);
+ent_status ent_attn_kv4_read(const void *k_codes, const void *k_meta, const void *v_codes,
+                             const void *v_meta, int pages, int page, const int32_t *block_table,
+                             int max_pages, const int32_t *start, const int32_t *new_lens, int B,
+                             int Hkv, int L, int d, int dtype, void *k, void *v, int32_t *bad,
+                             void *stream);
+size_t ent_attn_kv4_workspace_size(int B, int Hq, int Hkv, int L, int d, int dtype, int max_len,
+                                   int window, int sinks);
+ent_status ent_attn_kv4_fwd(const void *q, int B, int Hq, int Hkv, int L, int d, int dtype,
+                            float alpha, int window, int sinks, const void *k_codes,
+                            const void *k_meta, const void *v_codes, const void *v_meta, int pages,
+                            int page, const int32_t *block_table, int max_pages,
+                            const int32_t *start, const int32_t *new_lens, int max_len, void *o,
+                            float *tau, int32_t *bad, void *ws, size_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
