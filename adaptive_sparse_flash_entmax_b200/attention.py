@@ -57,15 +57,32 @@ def alloc_lists(q):
             torch.empty((B, H, N), dtype=torch.uint8, device=q.device))
 
 
+def _check_window(window, sinks, causal, lists):
+    if window is None:
+        if sinks:
+            raise ValueError("sinks need a window")
+        return
+    if not causal:
+        raise ValueError("a window needs causal=True")
+    if lists:
+        raise ValueError("support lists are not built under a window")
+    if window < 1 or sinks < 0:
+        raise ValueError(f"window must be at least 1 and sinks at least 0, not {window} and {sinks}")
+
+
 def entmax_attn_fwd(q, k, v, alpha: float = 1.5, causal: bool = False, *, with_iters=False,
-                    ws: torch.Tensor | None = None, out=None, otilde=None, lists=None):
+                    ws: torch.Tensor | None = None, out=None, otilde=None, lists=None,
+                    window: int | None = None, sinks: int = 0):
     """Forward: returns (o, tau, block_mask, iters_or_None).
 
     ``otilde``: a float32 tensor shaped like q to call ``ent_attn_fwd_otilde`` instead,
     which also fills it with sum_j g_ij v_j / sum_j g_ij (the backward's delta is then
     dO . otilde, see ``entmax_attn_bwd``).  ``lists``: the buffers of ``alloc_lists`` to
-    call ``ent_attn_fwd_lists``, which also records every row's (key, u) support list."""
+    call ``ent_attn_fwd_lists``, which also records every row's (key, u) support list.
+    ``window`` (with ``causal``): query i sees key j <= i when i - j < window or j < sinks
+    (``ent_attn_fwd_window``; ``otilde`` as above, no ``lists``)."""
     _check(q, k, v)
+    _check_window(window, sinks, causal, lists is not None)
     B, H, N, d = q.shape
     dt = _DTYPES[q.dtype]
     T = -(-N // capi.ent_attn_block_size()) if N else 0
@@ -82,7 +99,15 @@ def entmax_attn_fwd(q, k, v, alpha: float = 1.5, causal: bool = False, *, with_i
     args = (q.data_ptr(), k.data_ptr(), v.data_ptr(), B, H, N, d, dt, alpha, causal, o.data_ptr(),
             tau.data_ptr(), mask.data_ptr(), iters.data_ptr() if iters is not None else None)
     tail = (ws.data_ptr(), ws.numel(), _stream_handle(q.device))
-    if lists is not None:
+    if window is not None:
+        if otilde is not None:
+            _check_otilde(otilde, q)
+        big = 2 ** 31 - 1
+        with torch.cuda.device(q.device):
+            st = capi.ent_attn_fwd_window(*args[:9], min(window, big), min(sinks, big), *args[10:],
+                                          otilde.data_ptr() if otilde is not None else None, *tail)
+        _raise(st, "ent_attn_fwd_window")
+    elif lists is not None:
         if otilde is not None:
             raise ValueError("otilde and lists are separate forward variants")
         lk, lu, ln = lists
@@ -108,14 +133,17 @@ def _check_otilde(otilde, q):
 
 
 def entmax_attn_bwd(q, k, v, o, dout, tau, block_mask, alpha: float = 1.5, causal: bool = False,
-                    *, ws: torch.Tensor | None = None, out=None, otilde=None, lists=None):
+                    *, ws: torch.Tensor | None = None, out=None, otilde=None, lists=None,
+                    window: int | None = None, sinks: int = 0):
     """Backward: returns (dq, dk, dv).
 
     ``otilde``: the tensor a forward with ``otilde=`` filled; the call then goes to
     ``ent_attn_bwd_otilde`` (delta = dO . otilde, no delta pass over the keys).
     ``lists``: the support lists a forward with ``lists=`` filled; the call then goes to
-    ``ent_attn_bwd_lists`` (query tiles whose rows all have lists are done from them)."""
+    ``ent_attn_bwd_lists`` (query tiles whose rows all have lists are done from them).
+    ``window``, ``sinks``: the forward's (``ent_attn_bwd_window``)."""
     _check(q, k, v, dout)
+    _check_window(window, sinks, causal, lists is not None)
     B, H, N, d = q.shape
     dt = _DTYPES[q.dtype]
     if out is None:
@@ -129,7 +157,16 @@ def entmax_attn_bwd(q, k, v, o, dout, tau, block_mask, alpha: float = 1.5, causa
     tail = (dout.data_ptr(), tau.data_ptr(), block_mask.data_ptr(), B, H, N, d, dt, alpha, causal,
             dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ws.data_ptr(), ws.numel(),
             _stream_handle(q.device))
-    if lists is not None:
+    if window is not None:
+        if otilde is not None:
+            _check_otilde(otilde, q)
+        big = 2 ** 31 - 1
+        with torch.cuda.device(q.device):
+            st = capi.ent_attn_bwd_window(q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                          otilde.data_ptr() if otilde is not None else None,
+                                          *tail[:9], min(window, big), min(sinks, big), *tail[10:])
+        _raise(st, "ent_attn_bwd_window")
+    elif lists is not None:
         if otilde is not None:
             raise ValueError("otilde and lists are separate backward variants")
         lk, lu, ln = lists
@@ -169,21 +206,24 @@ class EntmaxAttention(torch.autograd.Function):
     (faster at high block sparsity, and the choice when activation memory is tight);
     ``delta="lists"`` keeps each row's support list (16 keys and u values, 128 bytes per
     row, bf16 inputs) and the backward does every query tile whose rows all have lists
-    from them (faster where nearly every row has at most 16 nonzeros)."""
+    from them (faster where nearly every row has at most 16 nonzeros).
+    ``window``, ``sinks``: as in entmax_attn_fwd (not with ``delta="lists"``)."""
 
     @staticmethod
-    def forward(ctx, q, k, v, alpha, causal, delta):
+    def forward(ctx, q, k, v, alpha, causal, delta, window=None, sinks=0):
         q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
         if delta not in ("otilde", "recompute", "lists"):
             raise ValueError(f"delta must be 'otilde', 'recompute' or 'lists', not {delta!r}")
+        _check_window(window, sinks, causal, delta == "lists")
         grad = any(ctx.needs_input_grad[:3])
         ot = (torch.empty(q.shape, dtype=torch.float32, device=q.device)
               if delta == "otilde" and grad else None)
         lists = alloc_lists(q) if delta == "lists" and grad else None
-        o, tau, mask, _ = entmax_attn_fwd(q, k, v, alpha, causal, otilde=ot, lists=lists)
+        o, tau, mask, _ = entmax_attn_fwd(q, k, v, alpha, causal, otilde=ot, lists=lists,
+                                          window=window, sinks=sinks)
         lk, lu, ln = lists if lists is not None else (None, None, None)
         ctx.save_for_backward(q, k, v, o, tau, mask, ot, lk, lu, ln)
-        ctx.alpha, ctx.causal = alpha, causal
+        ctx.alpha, ctx.causal, ctx.window, ctx.sinks = alpha, causal, window, sinks
         return o
 
     @staticmethod
@@ -191,13 +231,15 @@ class EntmaxAttention(torch.autograd.Function):
         q, k, v, o, tau, mask, ot, lk, lu, ln = ctx.saved_tensors
         lists = (lk, lu, ln) if lk is not None else None
         dq, dk, dv = entmax_attn_bwd(q, k, v, o, do.contiguous(), tau, mask, ctx.alpha, ctx.causal,
-                                     otilde=ot, lists=lists)
-        return dq, dk, dv, None, None, None
+                                     otilde=ot, lists=lists, window=ctx.window, sinks=ctx.sinks)
+        return dq, dk, dv, None, None, None, None, None
 
 
-def entmax_attention(q, k, v, alpha: float = 1.5, causal: bool = False, delta: str = "otilde"):
-    """Differentiable fused alpha-entmax attention (``delta``: see EntmaxAttention)."""
-    return EntmaxAttention.apply(q, k, v, alpha, causal, delta)
+def entmax_attention(q, k, v, alpha: float = 1.5, causal: bool = False, delta: str = "otilde",
+                     window: int | None = None, sinks: int = 0):
+    """Differentiable fused alpha-entmax attention (``delta``: see EntmaxAttention;
+    ``window``, ``sinks``: query i sees key j <= i when i - j < window or j < sinks)."""
+    return EntmaxAttention.apply(q, k, v, alpha, causal, delta, window, sinks)
 
 
 # ------------------------------------------------------------ row-wise entmax

@@ -82,6 +82,12 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.ent_entmax_rows_fwd.restype = ci
     lib.ent_entmax_rows_bwd.argtypes = [vp, vp, vp, ci, ci, ci, cf, vp, vp]
     lib.ent_entmax_rows_bwd.restype = ci
+    lib.ent_attn_fwd_window.argtypes = [vp, vp, vp, ci, ci, ci, ci, ci, cf, ci, ci, vp, vp, vp, vp,
+                                        vp, vp, sz, vp]
+    lib.ent_attn_fwd_window.restype = ci
+    lib.ent_attn_bwd_window.argtypes = [vp, vp, vp, vp, vp, vp, vp, ci, ci, ci, ci, ci, cf, ci, ci,
+                                        vp, vp, vp, vp, sz, vp]
+    lib.ent_attn_bwd_window.restype = ci
     lib.ent_attn_kv4_write.argtypes = [vp, vp, ci, ci, ci, ci, ci, vp, ci, vp, vp, vp, vp, vp, vp,
                                        ci, ci, vp, vp]
     lib.ent_attn_kv4_write.restype = ci
@@ -197,6 +203,19 @@ def ent_attn_bwd_lists(q, k, v, list_key, list_u, list_n, dout, tau, block_mask,
     return load().ent_attn_bwd_lists(q, k, v, list_key, list_u, list_n, dout, tau, block_mask, B,
                                      H, N, d, dtype, float(alpha), int(causal), dq, dk, dv, ws,
                                      ws_bytes, stream)
+
+
+def ent_attn_fwd_window(q, k, v, B, H, N, d, dtype, alpha, window, sinks, o, tau, block_mask,
+                        iters, otilde, ws, ws_bytes, stream) -> int:
+    return load().ent_attn_fwd_window(q, k, v, B, H, N, d, dtype, float(alpha), window, sinks, o,
+                                      tau, block_mask, iters, otilde, ws, ws_bytes, stream)
+
+
+def ent_attn_bwd_window(q, k, v, otilde, dout, tau, block_mask, B, H, N, d, dtype, alpha, window,
+                        sinks, dq, dk, dv, ws, ws_bytes, stream) -> int:
+    return load().ent_attn_bwd_window(q, k, v, otilde, dout, tau, block_mask, B, H, N, d, dtype,
+                                      float(alpha), window, sinks, dq, dk, dv, ws, ws_bytes,
+                                      stream)
 
 
 def ent_attn_kv4_write(k, v, B, Hkv, L, d, dtype, block_table, max_pages, start, new_lens, k_codes,

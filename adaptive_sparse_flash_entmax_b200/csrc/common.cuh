@@ -38,6 +38,29 @@ static_assert(sizeof(WsHeader) == 256, "workspace header is 256 bytes");
 enum Counter { kCtrQkBlocks = 0, kCtrPvBlocks = 1, kCtrPasses = 2, kCtrTiles = 3,
                kCtrBwdBlocks = 4, kCtrGvBlocks = 5, kCtrSkipped = 6, kCtrListEntries = 7 };
 
+// Sliding window with sinks (causal): query i sees key j iff j <= i and (i - j < window or
+// j < sinks).  The key blocks of query tile t that some row sees are the first `ns` (of the
+// sinks, as far as they lie before the window) and those from w0 to t.
+struct WinBlocks {
+    int ns, w0;
+    __host__ __device__ __forceinline__ WinBlocks(int window, int sinks, int t) {
+        const int first = t * kBlk - window + 1;   // first key of the tile's first row
+        w0 = first > 0 ? first / kBlk : 0;
+        const int sb = sinks / kBlk + (sinks % kBlk != 0);
+        ns = sb < w0 ? sb : w0;
+    }
+    __host__ __device__ __forceinline__ int count(int t) const { return ns + t + 1 - w0; }
+    __host__ __device__ __forceinline__ int block(int i) const { return i < ns ? i : w0 + i - ns; }
+    __host__ __device__ __forceinline__ bool has(int b) const { return b < ns || b >= w0; }
+};
+
+// Keys that query i sees.
+__host__ __device__ __forceinline__ int win_keys(int window, int sinks, int i) {
+    if (i < window) return i + 1;
+    const int before = i + 1 - window;   // keys before the window
+    return window + (sinks < before ? sinks : before);
+}
+
 __device__ __forceinline__ float load_f(const float* p, size_t i) { return p[i]; }
 __device__ __forceinline__ float load_f(const __nv_bfloat16* p, size_t i) {
     return __bfloat162float(p[i]);

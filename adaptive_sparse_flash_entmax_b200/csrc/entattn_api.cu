@@ -223,6 +223,18 @@ struct Lists {
     bool want = false;
 };
 
+// Sliding window of the *_window calls (want false otherwise).
+struct Window {
+    int window = 0, sinks = 0;
+    bool want = false;
+};
+
+ent_status check_window(const Window& w) {
+    if (w.want && (w.window < 1 || w.sinks < 0))
+        return fail(ENT_EINVAL, "window=%d must be at least 1 and sinks=%d at least 0", w.window, w.sinks);
+    return ENT_OK;
+}
+
 // Backward workspace of ent_attn_bwd_lists: the plain layout, then the per-tile flags
 // and the fp32 dK, dV accumulators of the list kernel.
 struct ListLayout {
@@ -243,8 +255,9 @@ ListLayout list_layout(int B, int H, int N, int d) {
 ent_status fwd_impl(const void* q, const void* k, const void* v, int B, int H, int N, int d,
                     int dtype, float alpha, int causal, void* o, float* tau, uint8_t* block_mask,
                     uint8_t* iters, float* otilde, bool want_otilde, void* ws, size_t ws_bytes,
-                    void* stream, const Lists& lists = Lists()) {
+                    void* stream, const Lists& lists = Lists(), const Window& win = Window()) {
     ent_status st = check_common(B, H, N, d, dtype, alpha, causal);
+    if (st == ENT_OK) st = check_window(win);
     if (st != ENT_OK) return st;
     if (lists.want && dtype != ENT_BF16)
         return fail(ENT_EUNSUPPORTED, "support lists are built by the bf16 forward only");
@@ -265,8 +278,10 @@ ent_status fwd_impl(const void* q, const void* k, const void* v, int B, int H, i
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const FwdLayout FL = fwd_layout(B, H, N, d);
     // (no tile of a shorter sequence runs the bound pass, so its statistics are not computed)
+    // (nor under a window, whose tiles visit few blocks: there the histogram start, the bound
+    // pass and the calibrated start are all off)
     const bool bound = dtype == ENT_BF16 && hist_budget() == 0 && bound_enabled() && !empty &&
-                       n_tiles(N) >= ent::kBoundMinBlocks;
+                       !win.want && n_tiles(N) >= ent::kBoundMinBlocks;
     // header, failure list (entries are tile + 1, 0 until written) and the per-head max |c|
     // start at 0, the per-head min R at all ones
     cudaError_t e = cudaMemsetAsync(ws, 0, bound ? FL.minr : (dtype == ENT_BF16 ? FL.maxc : kHdr), s);
@@ -288,14 +303,18 @@ ent_status fwd_impl(const void* q, const void* k, const void* v, int B, int H, i
     // far below their rounding; float32 outputs get 1e-6.
     a.ftol = dtype == ENT_F32 ? 1e-6f : 1e-5f;
     a.stol = dtype == ENT_F32 ? 4e-7f : 1e-6f;
-    a.hist_budget = hist_budget();
+    a.hist_budget = win.want ? 0 : hist_budget();
+    if (win.want) {   // (a window or sinks beyond the sequence are the sequence)
+        a.window = win.window < N ? win.window : N;
+        a.sinks = win.sinks < N ? win.sinks : N;
+    }
     if (dtype == ENT_BF16) {
         a.acc = accept_rule();
         a.verify_tol = verify_tol();
         a.spec = spec_enabled();
         a.fail_list = reinterpret_cast<int*>(static_cast<char*>(ws) + FL.fix);
     }
-    if (dtype == ENT_BF16 && hist_budget() == 0 && calib_enabled() && n_tiles(N) >= ent::kBoundMinBlocks) {
+    if (dtype == ENT_BF16 && hist_budget() == 0 && calib_enabled() && !win.want && n_tiles(N) >= ent::kBoundMinBlocks) {
         char* base = static_cast<char*>(ws);
         a.gap = reinterpret_cast<float*>(base + FL.gap);
         a.calib = reinterpret_cast<float*>(base + FL.calib);
@@ -324,8 +343,9 @@ ent_status bwd_impl(const void* q, const void* k, const void* v, const float* ot
                     bool want_otilde, const void* dout, const float* tau,
                     const uint8_t* block_mask, int B, int H, int N, int d, int dtype, float alpha,
                     int causal, void* dq, void* dk, void* dv, void* ws, size_t ws_bytes,
-                    void* stream, const Lists& lists = Lists()) {
+                    void* stream, const Lists& lists = Lists(), const Window& win = Window()) {
     ent_status st = check_common(B, H, N, d, dtype, alpha, causal);
+    if (st == ENT_OK) st = check_window(win);
     if (st != ENT_OK) return st;
     if (lists.want && dtype != ENT_BF16)
         return fail(ENT_EUNSUPPORTED, "support lists are built by the bf16 forward only");
@@ -367,6 +387,10 @@ ent_status bwd_impl(const void* q, const void* k, const void* v, const float* ot
     const int gm = gamma_mode(alpha, &a.gamma);
     a.scale = 1.f / sqrtf((float)d);
     a.cx = (alpha - 1.f) * a.scale;
+    if (win.want) {
+        a.window = win.window < N ? win.window : N;
+        a.sinks = win.sinks < N ? win.sinks : N;
+    }
     if (lists.want) {
         a.list_key = lists.key; a.list_u = lists.u; a.list_n = lists.n;
         a.tile_list = reinterpret_cast<uint8_t*>(base + LL.tiles);
@@ -438,6 +462,27 @@ ent_status ent_attn_bwd_otilde(const void* q, const void* k, const void* v, cons
                                void* stream) {
     return bwd_impl(q, k, v, otilde, true, dout, tau, block_mask, B, H, N, d, dtype, alpha, causal,
                     dq, dk, dv, ws, ws_bytes, stream);
+}
+
+ent_status ent_attn_fwd_window(const void* q, const void* k, const void* v, int B, int H, int N,
+                               int d, int dtype, float alpha, int window, int sinks, void* o,
+                               float* tau, uint8_t* block_mask, uint8_t* iters, float* otilde,
+                               void* ws, size_t ws_bytes, void* stream) {
+    Window w;
+    w.window = window; w.sinks = sinks; w.want = true;
+    return fwd_impl(q, k, v, B, H, N, d, dtype, alpha, 1, o, tau, block_mask, iters, otilde,
+                    otilde != nullptr, ws, ws_bytes, stream, Lists(), w);
+}
+
+ent_status ent_attn_bwd_window(const void* q, const void* k, const void* v, const float* otilde,
+                               const void* dout, const float* tau, const uint8_t* block_mask,
+                               int B, int H, int N, int d, int dtype, float alpha, int window,
+                               int sinks, void* dq, void* dk, void* dv, void* ws, size_t ws_bytes,
+                               void* stream) {
+    Window w;
+    w.window = window; w.sinks = sinks; w.want = true;
+    return bwd_impl(q, k, v, otilde, otilde != nullptr, dout, tau, block_mask, B, H, N, d, dtype,
+                    alpha, 1, dq, dk, dv, ws, ws_bytes, stream, Lists(), w);
 }
 
 int ent_attn_list_cap(void) { return ent::kListCap; }

@@ -23,6 +23,7 @@ struct FwdArgs {
     uint8_t* iters;        // nullable
     WsHeader* hdr;         // workspace header (status, counters)
     int BH, N, T, causal;
+    int window, sinks;     // window 0: none; else causal, at most N, sinks at most N
     int dr;                // head dimension of the tensors (row stride); the tensor-core
                            // kernels run d = 32 as d = 64 with zero-filled upper columns
     float alpha, gamma;    // gamma = 1/(alpha-1)
@@ -94,6 +95,7 @@ struct BwdArgs {
     float* dv_acc;         // workspace [BH][N][d]
     WsHeader* hdr;
     int BH, N, T, causal;
+    int window, sinks;     // as in FwdArgs
     int dr;                // head dimension of the tensors, as in FwdArgs
     float alpha, gamma, cx, scale;
 };

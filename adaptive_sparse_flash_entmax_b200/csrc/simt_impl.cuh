@@ -59,7 +59,9 @@ constexpr size_t simt_fwd_smem(int T) {
     return sizeof(float) * (128 * (D + 1) + 2 * kSub * D + kBins * 128 + 68) + (size_t)((T + 15) / 16) * 16;
 }
 
-template <typename TIn, int D, int GM>
+// WIN (every kernel): a sliding window with sinks; key blocks that no row of the query tile
+// sees are skipped and the others mask their elements.
+template <typename TIn, int D, int GM, bool WIN>
 __global__ void __launch_bounds__(128, 1) simt_fwd_kernel(FwdArgs a) {
     extern __shared__ __align__(16) unsigned char smem_raw[];
     float* Qs = reinterpret_cast<float*>(smem_raw);            // [128][D+1]
@@ -82,6 +84,9 @@ __global__ void __launch_bounds__(128, 1) simt_fwd_kernel(FwdArgs a) {
     const int last_row = min(t * kBlk + kBlk - 1, N - 1);
     const int nblk = a.causal ? t + 1 : T;
     const int key_end = !row_valid ? 0 : (a.causal ? i + 1 : N);   // admissible keys [0, key_end)
+    const int nkeys = !row_valid ? 0 : WIN ? win_keys(a.window, a.sinks, i) : key_end;
+    const WinBlocks wb(WIN ? a.window : 0, a.sinks, t);
+    auto seen = [&](int j) { return !WIN || j > i - a.window || j < a.sinks; };
     const float gamma = a.gamma, cx = a.cx;
 
     load_rows_f32<TIn, D>(Qs, D + 1, q, t * kBlk, kBlk, N, tid, 128);
@@ -100,6 +105,7 @@ __global__ void __launch_bounds__(128, 1) simt_fwd_kernel(FwdArgs a) {
     for (;; ++pass) {
         float F0 = 0.f, F1 = 0.f, F2 = 0.f;
         for (int b = 0; b < nblk; ++b) {
+            if (WIN && !wb.has(b)) continue;   // CTA-uniform; live[b] stays 0
             int any = 0;
             for (int sb = 0; sb < kBlk / kSub; ++sb) {
                 const int j0 = b * kBlk + sb * kSub;
@@ -114,7 +120,7 @@ __global__ void __launch_bounds__(128, 1) simt_fwd_kernel(FwdArgs a) {
                     float bm = -INFINITY;
 #pragma unroll
                     for (int jj = 0; jj < kSub; ++jj)
-                        if (jj < nv) bm = fmaxf(bm, __fmul_rn(cx, r[jj]));
+                        if (jj < nv && seen(j0 + jj)) bm = fmaxf(bm, __fmul_rn(cx, r[jj]));
                     if (bm > m) {
                         m = bm;
                         const int An = abs_bin(m);
@@ -123,7 +129,7 @@ __global__ void __launch_bounds__(128, 1) simt_fwd_kernel(FwdArgs a) {
                     }
 #pragma unroll
                     for (int jj = 0; jj < kSub; ++jj) {
-                        if (jj < nv) {
+                        if (jj < nv && seen(j0 + jj)) {
                             const int ab = abs_bin(__fmul_rn(cx, r[jj]));
                             if (ab >= A - (kBins - 1)) hist[(ab & (kBins - 1)) * 128 + tid] += 1u;
                         }
@@ -131,7 +137,7 @@ __global__ void __launch_bounds__(128, 1) simt_fwd_kernel(FwdArgs a) {
                 } else {
 #pragma unroll
                     for (int jj = 0; jj < kSub; ++jj) {
-                        if (jj < nv) {
+                        if (jj < nv && seen(j0 + jj)) {
                             const float u = __fmaf_rn(cx, r[jj], -st.tau);
                             float t0, t1, t2;
                             entmax_terms<GM>(u, gamma, t0, t1, t2);
@@ -148,7 +154,7 @@ __global__ void __launch_bounds__(128, 1) simt_fwd_kernel(FwdArgs a) {
         }
         if (pass == 0) {
             if (row_valid) {
-                hist_start<GM>(hist + tid, 128, A, m, key_end, a.alpha, gamma, ptab, st.lo, st.hi,
+                hist_start<GM>(hist + tid, 128, A, m, nkeys, a.alpha, gamma, ptab, st.lo, st.hi,
                                st.tau);
             }
         } else {
@@ -184,7 +190,7 @@ __global__ void __launch_bounds__(128, 1) simt_fwd_kernel(FwdArgs a) {
 #pragma unroll
                 for (int jj = 0; jj < kSub; ++jj) {
                     const float u = __fmaf_rn(cx, r[jj], -st.tau);
-                    const float p = (jj >= nv) ? 0.f : (sweep == 0) ? entmax_p<GM>(u, gamma) : entmax_g<GM>(u, gamma);
+                    const float p = (jj >= nv || !seen(j0 + jj)) ? 0.f : (sweep == 0) ? entmax_p<GM>(u, gamma) : entmax_g<GM>(u, gamma);
                     wsum += p;
 #pragma unroll
                     for (int c = 0; c < D; c += 4) {
@@ -215,7 +221,7 @@ __global__ void __launch_bounds__(128, 1) simt_fwd_kernel(FwdArgs a) {
     uint8_t* mrow = a.mask + ((size_t)bh * T + t) * T;
     for (int b = tid; b < T; b += 128) mrow[b] = (b < nblk) ? live[b] : 0;
     if (tid == 0) {
-        atomicAdd(&a.hdr->counters[kCtrQkBlocks], (unsigned long long)nblk * (npass + 1));
+        atomicAdd(&a.hdr->counters[kCtrQkBlocks], (unsigned long long)(WIN ? wb.count(t) : nblk) * (npass + 1));
         atomicAdd(&a.hdr->counters[kCtrPvBlocks], (unsigned long long)nlive);
         atomicAdd(&a.hdr->counters[kCtrPasses], (unsigned long long)npass);
         atomicAdd(&a.hdr->counters[kCtrTiles], 1ull);
@@ -230,7 +236,7 @@ constexpr size_t simt_bwd_dq_smem() {
     return sizeof(float) * (2 * 128 * (D + 1) + 2 * kSubB * D);
 }
 
-template <typename TIn, int D, int GM>
+template <typename TIn, int D, int GM, bool WIN>
 __global__ void __launch_bounds__(128, 1) simt_bwd_dq_kernel(BwdArgs a) {
     extern __shared__ __align__(16) unsigned char smem_raw[];
     float* Qs = reinterpret_cast<float*>(smem_raw);   // [128][D+1]
@@ -290,7 +296,9 @@ __global__ void __launch_bounds__(128, 1) simt_bwd_dq_kernel(BwdArgs a) {
                 const int nv = key_end - j0;
 #pragma unroll
                 for (int jj = 0; jj < kSubB; ++jj) {
-                    const float g = (jj < nv) ? entmax_g<GM>(__fmaf_rn(cx, r[jj], -tau), gamma) : 0.f;
+                    const int j = j0 + jj;
+                    const bool in = jj < nv && (!WIN || j > i - a.window || j < a.sinks);
+                    const float g = in ? entmax_g<GM>(__fmaf_rn(cx, r[jj], -tau), gamma) : 0.f;
                     if (phase == 0) {
                         sg += g;
                         sgdp = fmaf(g, dp[jj], sgdp);
@@ -330,7 +338,7 @@ constexpr size_t simt_bwd_dkv_smem() {
     return sizeof(float) * (2 * 128 * (D + 1) + 2 * kSubB * D + 2 * kSubB);
 }
 
-template <typename TIn, int D, int GM, int WHICH>
+template <typename TIn, int D, int GM, int WHICH, bool WIN>
 __global__ void __launch_bounds__(128, 1) simt_bwd_dkv_kernel(BwdArgs a) {
     extern __shared__ __align__(16) unsigned char smem_raw[];
     float* Ks = reinterpret_cast<float*>(smem_raw);   // [128][D+1]
@@ -382,7 +390,8 @@ __global__ void __launch_bounds__(128, 1) simt_bwd_dkv_kernel(BwdArgs a) {
 #pragma unroll
             for (int ii = 0; ii < kSubB; ++ii) {
                 const int irow = i0 + ii;
-                const bool ok = key_valid && irow < N && (!a.causal || j <= irow);
+                const bool ok = key_valid && irow < N && (!a.causal || j <= irow) &&
+                                (!WIN || irow - j < a.window || j < a.sinks);
                 const float u = __fmaf_rn(cx, r[ii], -tau_s[ii]);
                 float w;
                 const float* src;
@@ -414,7 +423,7 @@ __global__ void __launch_bounds__(128, 1) simt_bwd_dkv_kernel(BwdArgs a) {
 template <typename TIn, int D, int GM>
 cudaError_t simt_launch_fwd(const FwdArgs& a, cudaStream_t s) {
     const size_t sm = simt_fwd_smem<D>(a.T);
-    auto kern = simt_fwd_kernel<TIn, D, GM>;
+    auto kern = a.window ? simt_fwd_kernel<TIn, D, GM, true> : simt_fwd_kernel<TIn, D, GM, false>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
     if (e != cudaSuccess) return e;
     kern<<<dim3(a.T, a.BH), 128, sm, s>>>(a);
@@ -425,15 +434,15 @@ template <typename TIn, int D, int GM>
 cudaError_t simt_launch_bwd(const BwdArgs& a, cudaStream_t s) {
     {
         const size_t sm = simt_bwd_dq_smem<D>();
-        auto kern = simt_bwd_dq_kernel<TIn, D, GM>;
+        auto kern = a.window ? simt_bwd_dq_kernel<TIn, D, GM, true> : simt_bwd_dq_kernel<TIn, D, GM, false>;
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
         if (e != cudaSuccess) return e;
         kern<<<dim3(a.T, a.BH), 128, sm, s>>>(a);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
     const size_t sm = simt_bwd_dkv_smem<D>();
-    auto kv = simt_bwd_dkv_kernel<TIn, D, GM, 0>;
-    auto kk = simt_bwd_dkv_kernel<TIn, D, GM, 1>;
+    auto kv = a.window ? simt_bwd_dkv_kernel<TIn, D, GM, 0, true> : simt_bwd_dkv_kernel<TIn, D, GM, 0, false>;
+    auto kk = a.window ? simt_bwd_dkv_kernel<TIn, D, GM, 1, true> : simt_bwd_dkv_kernel<TIn, D, GM, 1, false>;
     cudaError_t e = cudaFuncSetAttribute(kv, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
     if (e != cudaSuccess) return e;
     e = cudaFuncSetAttribute(kk, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);

@@ -130,7 +130,9 @@ struct DqLayout {
     static size_t bytes(int T) { return (size_t)kList + 2 * (size_t)T + 16 + 1024; }
 };
 
-template <int D, int GM>
+// WIN (both kernels): a sliding window with sinks; the forward's block mask holds none of the
+// blocks outside it, and the blocks across its borders mask their elements here.
+template <int D, int GM, bool WIN>
 __global__ void __launch_bounds__(kThreads, 1)
 tc_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
                  const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -322,6 +324,11 @@ tc_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const float tau = row_valid ? a.tau[(size_t)bh * N + i] : 0.f;
         float* xch = reinterpret_cast<float*>(smem + L::kXch);   // [5][2][128]
         const float2 cx2 = make_float2(cx, cx), nt2 = make_float2(-tau, -tau);
+        // window: column c of the columns from key key0 on is seen iff c >= lo or c < sk,
+        // lo = wlo - key0, sk = sinks - key0
+        const int wlo = i - a.window + 1;
+        auto seen = [&](int key0, int c) { return c >= wlo - key0 || c < a.sinks - key0; };
+        auto seen_all = [&](int key0) { return wlo - key0 <= 0 || wlo <= a.sinks || a.sinks - key0 >= 64; };
         bool ok = true;
         // phase A: sum_j g and sum_j g dP
         float sg = 0.f, sgdp = 0.f;
@@ -341,10 +348,11 @@ tc_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&s_empty[p]);
-            const int nv = key_end - list[j] * kBlk - half * 64;
-            if (!__all_sync(0xffffffffu, nv >= 64)) {   // diagonal or ragged block
+            const int key0 = list[j] * kBlk + half * 64;
+            const int nv = key_end - key0;
+            if (!__all_sync(0xffffffffu, nv >= 64 && (!WIN || seen_all(key0)))) {   // diagonal, ragged or window edge
 #pragma unroll
-                for (int c = 0; c < 64; ++c) sa[c] = (c < nv) ? sa[c] : -INFINITY;
+                for (int c = 0; c < 64; ++c) sa[c] = (c < nv && (!WIN || seen(key0, c))) ? sa[c] : -INFINITY;
             }
             float2 a0 = make_float2(0.f, 0.f), b0 = a0, a1 = a0, b1 = a0;
 #pragma unroll
@@ -424,9 +432,9 @@ tc_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s_empty[p]);
                 const int nv = key_end - key0;   // valid columns of this thread: c < nv
-                if (!__all_sync(0xffffffffu, nv >= 64)) {   // diagonal or ragged block
+                if (!__all_sync(0xffffffffu, nv >= 64 && (!WIN || seen_all(key0)))) {   // diagonal, ragged or window edge
 #pragma unroll
-                    for (int c = 0; c < 64; ++c) sa[c] = (c < nv) ? sa[c] : -INFINITY;
+                    for (int c = 0; c < 64; ++c) sa[c] = (c < nv && (!WIN || seen(key0, c))) ? sa[c] : -INFINITY;
                 }
             }
             uint32_t whi[32];
@@ -531,7 +539,7 @@ struct DkvLayout {
     static size_t bytes(int T) { return (size_t)kList + 8 * (size_t)T + 1024; }
 };
 
-template <int D, int GM>
+template <int D, int GM, bool WIN>
 __global__ void __launch_bounds__(kThreads, 1)
 tc_bwd_dkv_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                   const __grid_constant__ CUtensorMap tm_q64, const __grid_constant__ CUtensorMap tm_do64,
@@ -586,11 +594,13 @@ tc_bwd_dkv_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         // tile per lane and step (the mask column is strided, so the loads go out in
         // parallel), up to two jobs each, placed by a warp prefix sum
         int n = 0;
-        for (int base = a.causal ? b : 0; base < T; base += 32) {
+        // (a key block past the sinks is seen by the queries of its window alone)
+        const int t_end = !WIN || b * kBlk < a.sinks ? T : min(T, (b * kBlk + kBlk + a.window - 2) / kBlk + 1);
+        for (int base = a.causal ? b : 0; base < t_end; base += 32) {
             const int t = base + lane;
             int c = 0, i0a = 0, i0b = 0;
             // live query tiles of this key block, except those the support-list kernel covered
-            if (t < T && a.mask[((size_t)bh * T + t) * T + b] &&
+            if (t < t_end && a.mask[((size_t)bh * T + t) * T + b] &&
                 !(a.tile_list && a.tile_list[(size_t)bh * T + t])) {
                 for (int h = 0; h < 2; ++h) {
                     const int i0 = t * kBlk + h * kSub;
@@ -739,7 +749,8 @@ tc_bwd_dkv_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             // column c is query i0 + 32*half + c: admissible iff i < N, key valid, key <= i if causal
             const int ib = i0 + half * 32;
             const int cmin = a.causal ? jkey - ib : 0;       // c >= cmin
-            const int cmax = min(32, N - ib);                // c < cmax
+            int cmax = min(32, N - ib);                      // c < cmax
+            if (WIN && jkey >= a.sinks) cmax = min(cmax, jkey + a.window - ib);
             const float* tcol = td + st * 128 + half * 32;   // tau, then delta 64 floats on
             if (!__all_sync(0xffffffffu, key_valid && cmin <= 0 && cmax >= 32)) {
                 // diagonal or ragged sub-tile: inadmissible columns get s = -inf (u < 0)
@@ -825,7 +836,7 @@ static cudaError_t launch_tc_bwd(const BwdArgs& a, cudaStream_t s, const CUtenso
     // m: q128, do128, k128, v128, q64, do64
     {
         const size_t sm = DqLayout<D>::bytes(a.T);
-        auto kern = tc_bwd_dq_kernel<D, GM>;
+        auto kern = a.window ? tc_bwd_dq_kernel<D, GM, true> : tc_bwd_dq_kernel<D, GM, false>;
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
         if (e != cudaSuccess) return e;
         kern<<<dim3(a.BH, a.T), kThreads, sm, s>>>(m[0], m[1], m[2], m[3], a);
@@ -837,7 +848,7 @@ static cudaError_t launch_tc_bwd(const BwdArgs& a, cudaStream_t s, const CUtenso
         if (e != cudaSuccess) return e;
     }
     const size_t sm = DkvLayout<D>::bytes(a.T);
-    auto kern = tc_bwd_dkv_kernel<D, GM>;
+    auto kern = a.window ? tc_bwd_dkv_kernel<D, GM, true> : tc_bwd_dkv_kernel<D, GM, false>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
     if (e != cudaSuccess) return e;
     kern<<<dim3(a.BH, a.T), kThreads, sm, s>>>(m[2], m[3], m[4], m[5], a);

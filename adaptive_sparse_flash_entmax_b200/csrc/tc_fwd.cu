@@ -143,6 +143,16 @@ struct SpecJob {
     }
 };
 
+// Window columns of query i in the columns from key `key0` on: column c is seen iff
+// c >= lo or c < sk (and c is not past the query).
+struct WinCols {
+    int lo, sk;
+    __device__ __forceinline__ WinCols(const FwdArgs& a, int i, int key0)
+        : lo(i - a.window + 1 - key0), sk(a.sinks - key0) {}
+    __device__ __forceinline__ bool sees(int c) const { return c >= lo || c < sk; }
+    __device__ __forceinline__ bool all(int n) const { return lo <= 0 || lo <= sk || sk >= n; }
+};
+
 // Bounded wait that ignores the abort flag (used to drain in-flight copies).
 __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
     const uint64_t t0 = globaltimer_ns();
@@ -155,7 +165,10 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
 
 // OT: also accumulate G.V (g = u^(gamma-1) as bf16 beside P in TMEM) and write
 // otilde = G.V / sum_j g, from which the backward takes delta without a pass over the keys.
-template <int D, int GM, bool OT>
+// WIN: a sliding window with sinks.  The tile's visible key blocks are known before the
+// first pass, so pass 0 takes them from the job list as a pass after the bound pass does;
+// blocks outside it keep block maxima of -inf and are never candidates.
+template <int D, int GM, bool OT, bool WIN>
 __global__ void __launch_bounds__(kThreads, 1)
 tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
               const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_c,
@@ -218,6 +231,7 @@ tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         use_bound = minr < 2.f * maxc;
     }
     const int nbj = use_bound ? (2 * nblk + 127) >> 7 : 0;   // 128-centroid jobs of the bound pass
+    const bool listed = use_bound || WIN;   // pass 0 visits the job list, not every block
 
     if (threadIdx.x == 0) {
         if (rep > 0)   // every phase of the previous tile is complete and nothing is in flight
@@ -236,7 +250,7 @@ tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         mbar_init(dec_bar, 1);
         mbar_init(mma_done, 1);
         misc->decision = 0;
-        misc->njobs = 0;
+        misc->njobs = WIN ? WinBlocks(a.window, a.sinks, t).count(t) : 0;
         misc->abort = 0;
         misc->inserts = 0;
         fence_barrier_init();
@@ -248,6 +262,12 @@ tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             tma_load_3d(smem + L::kQ + at * kAtom, &tm_q, at * 64, t * kBlk, bh, q_full);
     }
     for (int b = threadIdx.x; b < T; b += kThreads) { live[b] = 0; cand[b] = 0; }
+    if constexpr (WIN) {
+        const WinBlocks wb(a.window, a.sinks, t);
+        for (int i = threadIdx.x; i < wb.count(t); i += kThreads) job_list[i] = wb.block(i);
+        uint32_t* w = reinterpret_cast<uint32_t*>(bmw);
+        for (int i = threadIdx.x; i < nblk * 4; i += kThreads) w[i] = 0xFF80FF80u;   // -inf
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -258,7 +278,7 @@ tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         if (lane == 0) {
             int sj = 0, dj = 0, kind = kDecSolve;   // P.V-pass tiles, score-pass double slots loaded
             uint32_t dec_phase = 0;
-            bool ok = true, first = !use_bound, bound = use_bound;
+            bool ok = true, first = !listed, bound = use_bound;
             SpecJob spec;   // the next pass's first job, loaded before the decision
             // a score-pass job: K blocks b0 and b1 (b1 < 0: none) stacked in one double slot,
             // block h at rows 128h of each [256 rows x 64] atom (the bound pass loads blocks
@@ -345,7 +365,7 @@ tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             tc_fence_after();
             int sjob = 0, kind = kDecSolve;   // score-pass jobs issued (= double slots consumed)
             uint32_t dec_phase = 0;
-            bool first = !use_bound, bound = use_bound;
+            bool first = !listed, bound = use_bound;
             SpecJob spec;   // the next pass's first job, issued before the decision
             auto wait_tile = [&](int tt) { return mbar_wait(&kfull[tt % kSlots], (tt / kSlots) & 1, ab, 4); };
             auto issue_s = [&](int sb, int tt) {
@@ -465,6 +485,7 @@ tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         const int i = t * kBlk + row;
         const bool row_valid = i < N;
         const int key_end = !row_valid ? 0 : (a.causal ? i + 1 : N);
+        const int nkeys = !row_valid ? 0 : WIN ? win_keys(a.window, a.sinks, i) : key_end;
         const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
         const float gamma = a.gamma, cx = a.cx;
         // Row histograms in the (then idle) P region: [64 slots][128 rows] u32 words,
@@ -514,7 +535,7 @@ tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         sv.iters = 0;
         const int wi = warp - 2;                  // elementwise warp index 0..7
         int sjob = 0, pass = 0, nlive = 0;
-        long long qk_blocks = use_bound ? nbj : nblk, skipped = 0;
+        long long qk_blocks = use_bound ? nbj : WIN ? 0 : nblk, skipped = 0;
         bool ok = true;
         SpecJob spec;
         // a speculative job that is not used: wait for its S, then free the buffer unread
@@ -639,13 +660,13 @@ tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         for (;; ++pass) {
             float F0 = 0.f, F1 = 0.f, F2 = 0.f;
             int npj = nblk;
-            if (pass > 0 || use_bound) {
+            if (pass > 0 || listed) {
                 if (pass > 0)
                     for (int bb = ew; bb < nblk; bb += kEw) live[bb] = 0;
                 named_bar(1, kEw);   // also publishes job_list / njobs of this pass
                 npj = misc->njobs;
                 qk_blocks += npj;
-                if (pass == 0) skipped = nblk - npj;
+                if (pass == 0 && use_bound) skipped = nblk - npj;
             }
             // the speculative job issued after the previous pass: on a hit it is this pass's
             // first job (the next S buffer in sequence); on a miss its S is dropped
@@ -653,7 +674,7 @@ tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                 ok = ok && drop_job();
                 qk_blocks += spec.b1 >= 0 ? 2 : 1;
             }
-            spec.arm(a.spec && npj > 0, pass == 0 && !use_bound, npj, job_list);
+            spec.arm(a.spec && npj > 0, pass == 0 && !listed, npj, job_list);
             // jobs of two blocks (one 256-column S buffer); the buffer is released after
             // the second block's load
             for (int jj = 0; jj < npj && ok; jj += 2, ++sjob) {
@@ -664,7 +685,7 @@ tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
 #pragma unroll 1
                 for (int h = 0; h < nb2; ++h) {
                     const int bi = jj + h;      // block index within this pass
-                    const int b = (pass == 0 && !use_bound) ? bi : job_list[bi];
+                    const int b = (pass == 0 && !listed) ? bi : job_list[bi];
                     float s[64];
                     tmem_ld32(lane_base + sb * 256 + h * 128 + c0, &s[0]);
                     tmem_ld32(lane_base + sb * 256 + h * 128 + c0 + 32, &s[32]);
@@ -676,10 +697,12 @@ tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                         if (lane == 0) mbar_arrive(&s_empty2[sb]);
                     }
                     const int nv = key_end - b * kBlk - c0;   // valid columns of this thread: c < nv
-                    const bool full_blk = __all_sync(0xffffffffu, nv >= 64);
+                    const WinCols wc(a, i, b * kBlk + c0);
+                    const bool full_blk = __all_sync(0xffffffffu, nv >= 64 && (!WIN || wc.all(64)));
                     if (!full_blk) {
 #pragma unroll
-                        for (int c = 0; c < 64; ++c) s[c] = (c < nv) ? s[c] : -INFINITY;
+                        for (int c = 0; c < 64; ++c)
+                            s[c] = (c < nv && (!WIN || wc.sees(c))) ? s[c] : -INFINITY;
                     }
                     if (pass == 0) {
                         float m0 = s[0], m1 = s[1], m2 = s[2], m3 = s[3];
@@ -789,7 +812,7 @@ tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                     // m - (the gap of the nearest sampled row) when the start is calibrated
                     const float mr = fmaxf(m, m_other);
                     sv.lo = mr - 1.f;
-                    sv.hi = fmaxf(sv.lo, mr - exp2f((1.f - a.alpha) * __log2f((float)key_end)));
+                    sv.hi = fmaxf(sv.lo, mr - exp2f((1.f - a.alpha) * __log2f((float)nkeys)));
                     sv.tau = 0.5f * (sv.lo + sv.hi);
                     if (a.gap) {
                         const int sr = min(max((int)(((long long)(i + 1) * kCalRows + N / 2) / N) - 1, 0), kCalRows - 1);
@@ -885,7 +908,8 @@ tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                 if (!(ok = mbar_wait(&s_full[sb], (li / SB) & 1, ab, 9))) break;
                 tc_fence_after();
                 const int nv = key_end - b * kBlk - c0;   // valid columns of this thread: c < nv
-                const bool full_blk = __all_sync(0xffffffffu, nv >= 64);
+                const WinCols wc(a, i, b * kBlk + c0);
+                const bool full_blk = __all_sync(0xffffffffu, nv >= 64 && (!WIN || wc.all(64)));
                 const float2 cx2 = make_float2(cx, cx), nt2 = make_float2(-sv.tau, -sv.tau);
                 uint32_t nzb = 0u;   // OR of this thread's bf16 p bits: nonzero iff some p > 0
                 // two rounds of 32 keys, each loaded, turned into P (and G) and stored over its
@@ -899,7 +923,8 @@ tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                     reg_fence<32>(s);
                     if (!full_blk) {
 #pragma unroll
-                        for (int c = 0; c < 32; ++c) s[c] = (32 * hc + c < nv) ? s[c] : -INFINITY;
+                        for (int c = 0; c < 32; ++c)
+                            s[c] = (32 * hc + c < nv && (!WIN || wc.sees(32 * hc + c))) ? s[c] : -INFINITY;
                     }
                     uint32_t pk[16];
                     [[maybe_unused]] uint32_t gk[16];
@@ -1434,7 +1459,8 @@ static cudaError_t launch_tc_fwd(const CUtensorMap& mq, const CUtensorMap& mk,
         if (e != cudaSuccess) return e;
     }
     const size_t sm = Layout<D>::bytes(a.T);
-    auto kern = a.otilde ? tc_fwd_kernel<D, GM, true> : tc_fwd_kernel<D, GM, false>;
+    auto kern = a.window ? (a.otilde ? tc_fwd_kernel<D, GM, true, true> : tc_fwd_kernel<D, GM, false, true>)
+                         : (a.otilde ? tc_fwd_kernel<D, GM, true, false> : tc_fwd_kernel<D, GM, false, false>);
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
     if (e != cudaSuccess) return e;
     kern<<<dim3(a.BH, a.T), kThreads, sm, s>>>(mq, mk, mv, mc, a);

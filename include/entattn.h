@@ -214,6 +214,30 @@ ent_status ent_attn_bwd_lists(const void *q, const void *k, const void *v,
                               void *ws, size_t ws_bytes, void *stream);
 
 /*
+ * Causal attention with a sliding window and sinks: query i sees key j iff
+ *     j <= i and (i - j < window or j < sinks),
+ * window >= 1 (each query sees at least itself), sinks >= 0; values beyond N are N.  The
+ * pages of the method describe full and causal rows only.  Everything else is as
+ * ent_attn_fwd / ent_attn_bwd have it, with the rows' sums over the visible keys: same
+ * outputs (block_mask entries of blocks that no row sees are 0), workspace sizes, limits
+ * and counters.  The forward visits the key blocks that some row of a query tile sees, so
+ * its work grows with N * (window + sinks) instead of N^2; it starts every row from the
+ * bracket's midpoint.  otilde (nullable) as in ent_attn_fwd_otilde / ent_attn_bwd_otilde:
+ * the forward fills it, the backward then takes delta from it; with NULL the backward
+ * recomputes delta.  The backward's window and sinks must be the forward's.
+ */
+ent_status ent_attn_fwd_window(const void *q, const void *k, const void *v,
+                               int B, int H, int N, int d, int dtype, float alpha,
+                               int window, int sinks, void *o, float *tau,
+                               uint8_t *block_mask, uint8_t *iters, float *otilde,
+                               void *ws, size_t ws_bytes, void *stream);
+ent_status ent_attn_bwd_window(const void *q, const void *k, const void *v, const float *otilde,
+                               const void *dout, const float *tau, const uint8_t *block_mask,
+                               int B, int H, int N, int d, int dtype, float alpha,
+                               int window, int sinks, void *dq, void *dk, void *dv,
+                               void *ws, size_t ws_bytes, void *stream);
+
+/*
  * Backward without a workspace argument.  The pages have no counterpart: this
  * is a library convenience.  It computes exactly what ent_attn_bwd computes
  * (same kernels, same arguments minus ws / ws_bytes) for callers that cannot

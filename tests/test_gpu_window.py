@@ -1,0 +1,209 @@
+"""Windowed attention with sinks on the GPU against the definition in 64 bits.
+
+Tolerances.  float32: those of the float32 path (1e-4 on O); its gradients are float sums of terms with tau off by
+at most 1e-6: 1e-4 relative (2-norm).  bfloat16: on each element of O, P rounded once (2^-8 of sum p |v|), the
+forward's own bound |sum p - 1| <= 1e-4 (times max |v|), and the output's rounding (2^-8 |o|); on gradients, two
+roundings of 2^-8 at most on each term (the operand P or dS, and the output) and 2e-3 for tau and delta: 1e-2
+relative (2-norm)."""
+import pytest
+import torch
+
+from adaptive_sparse_flash_entmax_b200 import attention as A
+from adaptive_sparse_flash_entmax_b200 import entmax_attention
+
+pytestmark = pytest.mark.gpu
+
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+GRAD = {"f32": 1e-4, "bf16": 1e-2}
+
+
+def visible(N, window, sinks):
+    i = torch.arange(N, device="cuda")
+    back = i[:, None] - i[None, :]
+    return (back >= 0) & ((back < window) | (i[None, :] < sinks))
+
+
+def forward64(q, k, v, alpha, window, sinks):
+    """(o, p, u) in float64."""
+    gamma = 1 / (alpha - 1)
+    x = (alpha - 1) * (q @ k.transpose(-1, -2)) / q.shape[-1] ** 0.5
+    x = x.masked_fill(~visible(q.shape[-2], window, sinks), float("-inf"))
+    hi = x.amax(-1, keepdim=True)
+    lo = hi - 1
+    for _ in range(56):
+        mid = (lo + hi) / 2
+        up = torch.relu(x - mid).pow(gamma).sum(-1, keepdim=True) > 1
+        lo, hi = torch.where(up, mid, lo), torch.where(up, hi, mid)
+    u = torch.relu(x - (lo + hi) / 2)
+    p = u ** gamma
+    return p @ v, p, u
+
+
+def reference(q, k, v, do, alpha, window, sinks):
+    q, k, v, do = (t.double() for t in (q, k, v, do))
+    gamma, scale = 1 / (alpha - 1), q.shape[-1] ** -0.5
+    o, p, u = forward64(q, k, v, alpha, window, sinks)
+    g = torch.where(u > 0, u ** (gamma - 1), torch.zeros_like(u))
+    dp = do @ v.transpose(-1, -2)
+    ds = g * (dp - (g * dp).sum(-1, keepdim=True) / g.sum(-1, keepdim=True))
+    return o, ds @ k * scale, ds.transpose(-1, -2) @ q * scale, p.transpose(-1, -2) @ do, p @ v.abs()
+
+
+def make(B, H, N, d, dtype, seed, beta=2.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    q, k, v, do = (torch.randn(B, H, N, d, generator=g, device="cuda") for _ in range(4))
+    return [t.to(DT[dtype]) for t in (beta * q, k, v, do)]
+
+
+def check(got, want, dtype, v, grads=("dq", "dk", "dv")):
+    o, pv = want[0], want[4]
+    err = (got[0].double() - o).abs()
+    if dtype == "f32":
+        tol = torch.full_like(o, 1e-4)
+    else:
+        tol = 2.0 ** -8 * pv + 1e-4 * v.double().abs().amax() + 1e-5
+        tol = tol + 2.0 ** -8 * (o.abs() + tol)
+    assert bool((err <= tol).all()), f"o off by {float((err - tol).max()):.3g} too much"
+    for name, a, b in zip(("dq", "dk", "dv"), got[1:], want[1:4]):
+        if name not in grads:
+            continue
+        norm = float(b.norm())
+        rel = float((a.double() - b).norm()) / norm if norm else float(a.double().norm())
+        assert rel <= GRAD[dtype], f"{name} off by {rel:.3g}"
+
+
+def grads_of(q, k, v, do, alpha, window, sinks, delta):
+    q, k, v = (t.clone().requires_grad_() for t in (q, k, v))
+    o = entmax_attention(q, k, v, alpha, True, delta, window, sinks)
+    return [o.detach(), *torch.autograd.grad(o, (q, k, v), do)]
+
+
+SHAPES = [  # B, H, N, d, window, sinks
+    (1, 1, 1, 64, 1, 0),
+    (2, 1, 5, 32, 2, 1),
+    (1, 2, 127, 64, 64, 0),
+    (1, 2, 128, 128, 127, 4),
+    (2, 2, 129, 64, 128, 1),
+    (1, 3, 300, 128, 129, 16),
+    (1, 2, 515, 64, 1, 0),
+    (1, 2, 515, 64, 3, 130),
+    (1, 2, 515, 32, 200, 300),
+    (1, 1, 700, 128, 1, 700),
+    (1, 2, 900, 64, 256, 4),
+    (1, 1, 900, 128, 5000, 3),
+]
+
+
+@pytest.mark.parametrize("delta", ["otilde", "recompute"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,H,N,d,window,sinks", SHAPES)
+def test_forward_and_gradients(B, H, N, d, window, sinks, dtype, delta):
+    q, k, v, do = make(B, H, N, d, dtype, N + window)
+    got = grads_of(q, k, v, do, 1.5, window, sinks, delta)
+    # a row that sees one key has a constant output: dq is rounding there (dS = 0 for every row when window 1, no sinks)
+    check(got, reference(q, k, v, do, 1.5, window, sinks), dtype, v,
+          ("dv",) if window == 1 and sinks == 0 else ("dq", "dk", "dv"))
+    if window == 1 and sinks == 0:
+        # o = p v with the one p: in bfloat16 it is 1 (|p - 1| <= 1e-4 rounds to 1); in float32 it stops at
+        # |p - 1| <= 1e-6 or a step of 4e-7 max(1, |tau|), twice that in p, plus 2^-23 |tau| for u = x - tau, |tau| < 6
+        off = 0 if dtype == "bf16" else 6 * (2 * 4e-7 + 2.0 ** -22)
+        assert bool(((got[0].double() - v.double()).abs() <= off * v.double().abs()).all())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("alpha", [1.25, 4 / 3, 1.7, 2.0])
+def test_alphas(alpha, dtype):
+    q, k, v, do = make(1, 2, 400, 64, dtype, 3)
+    got = grads_of(q, k, v, do, alpha, 150, 8, "otilde")
+    # from gamma = 1/(alpha-1) < 1.5 on, g = u^(gamma-1) jumps or is steep at the border of the support, where the
+    # rounding of a score decides it: dq and dk are held to the formula for the others
+    check(got, reference(q, k, v, do, alpha, 150, 8), dtype, v, ("dv",) if alpha > 1.6 else ("dq", "dk", "dv"))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_a_window_over_everything_is_causal_attention(dtype):
+    q, k, v, do = make(1, 2, 450, 64, dtype, 4)
+    o, tau, mask, _ = A.entmax_attn_fwd(q, k, v, 1.5, True)
+    ow, tw, mw, _ = A.entmax_attn_fwd(q, k, v, 1.5, True, window=10 ** 12, sinks=7)
+    assert torch.equal(o, ow) and torch.equal(tau, tw) and torch.equal(mask, mw)
+    for a, b in zip(A.entmax_attn_bwd(q, k, v, o, do, tau, mask, 1.5, True),
+                    A.entmax_attn_bwd(q, k, v, None, do, tau, mask, 1.5, True, window=450)):
+        assert torch.equal(a, b)
+
+
+def test_block_mask_and_work_stay_inside():
+    """No block outside the window or the sinks is live or visited."""
+    N, W, S = 2000, 256, 3
+    q, k, v, _ = make(1, 2, N, 64, "bf16", 5)
+    ws = A.workspace(1 << 24, q.device)
+    _, _, mask, _ = A.entmax_attn_fwd(q, k, v, 1.5, True, window=W, sinks=S, ws=ws)
+    T = mask.shape[-1]
+    seen = torch.nn.functional.pad(visible(N, W, S), (0, T * 128 - N, 0, T * 128 - N)).view(T, 128, T, 128).any(3).any(1)
+    assert not bool(mask[:, :, ~seen].any())
+    assert bool(mask[:, :, torch.arange(T), torch.arange(T)].all())
+    visited, passes = A.read_status(ws)[0], A.read_status(ws)[2]
+    assert visited <= int(seen.sum()) * 2 * 26 and passes >= 2 * T
+
+
+def test_against_differences():
+    """The gradients against central differences of the 64-bit forward (its error is eps^2 and 1e-16 / eps)."""
+    q, k, v, do = make(1, 1, 140, 32, "f32", 6, beta=1.0)
+    got = grads_of(q, k, v, do, 1.5, 20, 2, "recompute")
+    base = [t.double() for t in (q, k, v)]
+    g = torch.Generator(device="cuda").manual_seed(7)
+    for n in range(3):
+        for _ in range(4):
+            step = torch.randn(base[n].shape, generator=g, device="cuda", dtype=torch.float64)
+            eps = 1e-5
+            ends = []
+            for s in (eps, -eps):
+                moved = list(base)
+                moved[n] = base[n] + s * step
+                ends.append(float((forward64(*moved, 1.5, 20, 2)[0] * do.double()).sum()))
+            want = (ends[0] - ends[1]) / (2 * eps)
+            have = float((got[1 + n].double() * step).sum())
+            # f's second derivative jumps where a key enters the support (eps of them in reach): 1e-4 of the terms
+            assert abs(have - want) <= 2e-4 * float((got[1 + n].double() * step).norm()) * 10
+
+
+def test_graph_stream_and_repeats():
+    q, k, v, do = make(1, 2, 600, 64, "bf16", 8)
+    first = grads_of(q, k, v, do, 1.5, 200, 4, "otilde")
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        again = grads_of(q, k, v, do, 1.5, 200, 4, "otilde")
+    torch.cuda.current_stream().wait_stream(stream)
+    assert all(torch.equal(a, b) for a, b in zip(first, again))
+    ot = torch.empty(q.shape, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, tau, mask, _ = A.entmax_attn_fwd(q, k, v, 1.5, True, otilde=ot, window=200, sinks=4)
+        outs = [o, *A.entmax_attn_bwd(q, k, v, None, do, tau, mask, 1.5, True, otilde=ot, window=200, sinks=4)]
+    graph.replay()
+    assert all(torch.equal(a, b) for a, b in zip(first, outs))
+    new = make(1, 2, 600, 64, "bf16", 9)
+    for t, n in zip((q, k, v, do), new):
+        t.copy_(n)
+    graph.replay()
+    assert all(torch.equal(a, b) for a, b in zip(grads_of(*new, 1.5, 200, 4, "otilde"), outs))
+
+
+def test_long_window():
+    """Over 64 tiles, where full attention would calibrate its start and bound its blocks: sampled rows."""
+    N, W, S = 9001, 700, 5
+    q, k, v, _ = make(1, 1, N, 64, "bf16", 10)
+    o = entmax_attention(q, k, v, 1.5, True, window=W, sinks=S)[0, 0]
+    seen = visible(N, W, S)
+    for i in (0, 1, 699, 700, 705, 4500, 8192, 9000):
+        kk, vv = k[0, 0][seen[i]].double(), v[0, 0][seen[i]].double()
+        x = 0.5 * (kk @ q[0, 0, i].double()) / 8
+        hi = x.max()
+        lo = hi - 1
+        for _ in range(56):
+            mid = (lo + hi) / 2
+            lo, hi = (mid, hi) if float(torch.relu(x - mid).square().sum()) > 1 else (lo, mid)
+        p = torch.relu(x - lo).square()
+        want = p @ vv
+        tol = 2.0 ** -8 * (p @ vv.abs()) + 1e-4 * vv.abs().max() + 1e-5
+        assert bool(((o[i].double() - want).abs() <= tol + 2.0 ** -8 * (want.abs() + tol)).all())
