@@ -14,7 +14,8 @@ _DTYPES = {torch.float32: capi.ENT_F32, torch.bfloat16: capi.ENT_BF16}
 
 
 def _stream_handle(device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+    """The current stream of a CUDA tensor's device, without the Stream object around it (0.1 us, not 3)."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 # The library launches on the calling thread's current CUDA device; every call below

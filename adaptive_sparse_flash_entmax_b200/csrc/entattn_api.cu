@@ -732,26 +732,33 @@ ent_status check_kv4(ent::Kv4Args& a, const void* kc, const void* km, const void
     return ENT_OK;
 }
 
-// Workspace of the attention: per row and chunk the maximum and the count, then the
-// candidates' scores and keys.  The rows of one key head share a scores CTA, 8, 16 or 32
-// of them (matrix instructions are 8 queries wide; float32 rows at d = 128 take two parts
-// each and stay at 16).
+// Workspace of the attention: per row and run of chunks the maximum and the count, then the
+// candidates (score and key).  The rows of one key head share a scores warp, 4, 8, 16 or 32
+// of them (the product is 8 queries wide; a warp of 4 looks its scores through with twice the
+// lanes a row; float32 rows at d = 128 take two parts each and stay at 16).
 struct Kv4Layout {
-    int ntile, chunk, nchunk;
-    size_t n, x, j, total;
+    int block, chunk, nchunk, nsplit, cap;
+    size_t n, cand, total;
 };
 
 bool kv4_layout(const ent::Kv4Geom& g, long long rows, int group, int d, int dtype, Kv4Layout* l) {
     const long long per = (long long)g.L * group;
-    l->ntile = per <= 8 ? 1 : per <= 16 || (dtype == ENT_F32 && d == 128) ? 2 : 4;
-    if (per > 8ll * l->ntile * 65535 || rows > 0x7fffffffll) return false;
-    l->chunk = ent::kv4_chunk_keys(l->ntile);
+    l->block = per <= 4 ? 4 : per <= 8 ? 8 : per <= 16 || (dtype == ENT_F32 && d == 128) ? 16 : 32;
+    if (per > 65535ll * l->block || rows > 0x7fffffffll) return false;
+    l->chunk = ent::kv4_chunk_keys(l->block);
     l->nchunk = ent::kv4_chunks(g, l->chunk);
-    const size_t lists = (size_t)rows * l->nchunk;
+    // runs: enough warps for two rounds of 16 on each SM, no more (a longer run's later chunks
+    // are filtered by a higher maximum, and its prologue is paid once)
+    const long long blocks = (rows / (per > 0 ? per : 1)) * ((per + l->block - 1) / l->block);
+    long long want = blocks > 0 ? (2 * 16 * 148 + blocks - 1) / blocks : 1;
+    if (want > ent::kKvMaxSplit) want = ent::kKvMaxSplit;
+    if (want > l->nchunk) want = l->nchunk > 0 ? l->nchunk : 1;
+    l->nsplit = (int)want;
+    l->cap = ent::kv4_run(l->nchunk, l->nsplit) * l->chunk;
+    const size_t lists = (size_t)rows * l->nsplit;
     l->n = round_up(lists * 4, 256);
-    l->x = l->n + round_up(lists * 4, 256);
-    l->j = l->x + round_up(lists * l->chunk * 4, 256);
-    l->total = l->j + round_up(lists * l->chunk * 2, 256);
+    l->cand = l->n + round_up(lists * 4, 256);
+    l->total = l->cand + round_up(lists * l->cap * 8, 256);
     return true;
 }
 
@@ -845,12 +852,12 @@ ent_status ent_attn_kv4_fwd(const void* q, int B, int Hq, int Hkv, int L, int d,
     a.alpha = alpha;
     const int gm = gamma_mode(alpha, &a.gamma);
     a.cx = (alpha - 1.f) / sqrtf((float)d);
-    a.ntile = l.ntile; a.chunk = l.chunk; a.nchunk = l.nchunk;
+    a.block = l.block; a.chunk = l.chunk; a.nchunk = l.nchunk;
+    a.nsplit = l.nsplit; a.cap = l.cap;
     char* base = static_cast<char*>(ws);
-    a.chunk_max = reinterpret_cast<float*>(base);
-    a.chunk_n = reinterpret_cast<int*>(base + l.n);
-    a.cand_x = reinterpret_cast<float*>(base + l.x);
-    a.cand_j = reinterpret_cast<uint16_t*>(base + l.j);
+    a.split_max = reinterpret_cast<float*>(base);
+    a.split_n = reinterpret_cast<int*>(base + l.n);
+    a.cand = reinterpret_cast<int2*>(base + l.cand);
     cudaError_t e = ent::kv4_attn(a, d, dtype == ENT_BF16, gm, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? ENT_OK : cuda_fail(e, "cache attention launch");
 }

@@ -139,14 +139,15 @@ struct Kv4Args {
     void* o;
     float* tau;                 // nullable [B][Hkv * group][L], x units
     float alpha, gamma, cx;     // as in FwdArgs
-    int ntile;                  // query rows of a scores CTA / 8 (1, 2 or 4)
+    int block;                  // query rows of a scores warp (4, 8, 16 or 32)
     int chunk, nchunk;          // keys of a chunk, chunks of a call
-    float* chunk_max;           // workspace: [rows][nchunk], rows = B Hkv L group
-    int* chunk_n;               //            [rows][nchunk]
-    float* cand_x;              //            [rows][nchunk][chunk]
-    uint16_t* cand_j;           //            [rows][nchunk][chunk]
+    int nsplit, cap;            // runs of chunks, one scores warp each; keys of the longest run
+    float* split_max;           // workspace: [rows][nsplit], rows = B Hkv L group
+    int* split_n;               //            [rows][nsplit]
+    int2* cand;                 //            [rows][nsplit][cap]: score bits, key
 };
-__host__ __device__ constexpr int kv4_chunk_keys(int ntile) { return ntile == 4 ? 256 : 512; }
+__host__ __device__ constexpr int kv4_chunk_keys(int block) { return block == 32 ? 32 : 64; }
+constexpr int kKvMaxSplit = 1024;
 cudaError_t kv4_write(const Kv4Args& a, int d, bool bf16, cudaStream_t s);
 cudaError_t kv4_read(const Kv4Args& a, int d, bool bf16, cudaStream_t s);
 cudaError_t kv4_attn(const Kv4Args& a, int d, bool bf16, int gm, cudaStream_t s);

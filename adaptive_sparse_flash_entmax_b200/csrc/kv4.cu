@@ -168,35 +168,50 @@ __global__ void __launch_bounds__(kKvThreads) kv4_read_kernel(const Kv4Args a) {
 }
 
 // ------------------------------------------------------------------ scores
-// One CTA per (chunk of C keys, block of R = 8 NT rows, sequence and key head).  The rows
-// are the new tokens' queries of all heads that share the key head, row = l * group + head
-// of the group.  Keys are the M = 16 rows of an m16n8k16 product and the queries its 8
-// columns; the contraction index is permuted so that a lane's four A registers are its own
-// words of two keys, masked: a nibble at bits 0-3 of a half is code * 2^-24 (a subnormal,
-// which the product takes exactly), one at bits 4-7 is 16 times that, and the queries'
-// other operand carries the 1/16.  So 8 codes cost four ANDs and a shift, and the product
-// is exact in the codes.  The pair (scale, zero) of each group comes in afterwards:
-//     q.k = sum_groups scale * (codes . q) + zero * sum q.
+// A warp per (run of chunks of C keys, block of R rows, sequence and key head): four warps a
+// CTA that share nothing.  The rows are the new tokens' queries of all heads that share the
+// key head, row = l * group + head of the group.  Keys are the M = 16 rows of an m16n8k16
+// product and the queries its 8 columns; the contraction index is permuted so that a lane's
+// four A registers are its own words of two keys, masked: a nibble at bits 0-3 of a half is
+// code * 2^-24 (a subnormal, which the product takes exactly), one at bits 4-7 is 16 times
+// that, and the queries' other operand carries the 1/16.  So 8 codes cost four ANDs and a
+// shift, and the product is exact in the codes.  The pair (scale, zero) of each group comes
+// in afterwards:
+//     q.k = sum_groups scale * (codes . q) + zero * sum q,
+// the second sum as a product too: a lane's pair of group c is two elements of an A operand,
+// met by (0, sum q of group c) in three bf16 parts (24 bits).
 // The queries are fp16, scaled per row by a power of two so that the largest lies in
 // [2^14, 2^15): exact for bf16 values down to 2^-31 of the largest, below which the
 // rounding is 2^-39 of it; a float32 row is the sum of two such halves (22 bits).
-struct ChunkOut {
-    float* x;      // [rows][chunks][C] scores of the chunk's candidates, in key order
-    uint16_t* j;   // their key - the chunk's first key
-    float* m;      // [rows][chunks] maximum (NaN where a visible score is NaN or +inf)
-    int* n;        // [rows][chunks] candidates
-};
-
+// The scores of a chunk pass through the warp's shared memory (queries by keys), where 32/R
+// lanes a row take their maximum and the candidates above the run's maximum so far - 1.
 __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                           uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void mma_16816_bf(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                             uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_1688_bf(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(b0));
+}
 
 __device__ __forceinline__ uint32_t pack_half(float a, float b) {
     const __half2 h = __floats2half2_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&h);
+}
+// x rounded to bf16, in the upper half of a word; what is left stays in x
+__device__ __forceinline__ uint32_t bf16_part(float& x) {
+    const __nv_bfloat16 h = __float2bfloat16_rn(x);
+    x -= __bfloat162float(h);
+    return (uint32_t)__bfloat16_as_ushort(h) << 16;
 }
 
 // G consecutive 4-byte words (one load)
@@ -213,41 +228,37 @@ __device__ __forceinline__ void load_words(const uint32_t* p, uint32_t (&w)[G]) 
     }
 }
 
-template <typename T, int D, int NT>
-__global__ void __launch_bounds__(kKvThreads) kv4_scores_kernel(const Kv4Args a) {
-    constexpr int G = D / kKvGroup, C = kv4_chunk_keys(NT), R = 8 * NT;
-    constexpr int kStride = C + 4;   // spreads a warp's 8 keys x 4 row pairs over the banks
-    constexpr int kTiles = C / kKvTile / (kKvThreads / 32);   // tiles of one warp
-    constexpr int U = kTiles < 4 ? kTiles : 4;                // of them in flight together
+constexpr int kScoreThreads = 128;
+constexpr int kScoreWarps = kScoreThreads / 32;
+
+// R: rows of a block (4, 8, 16 or 32), in NT products of 8 columns.
+template <typename T, int D, int R>
+__global__ void __launch_bounds__(kScoreThreads, R <= 8 ? 4 : R <= 16 ? 3 : 2) kv4_scores_kernel(const Kv4Args a) {
+    constexpr int G = D / kKvGroup, NT = R <= 8 ? 1 : R / 8, C = kv4_chunk_keys(R), U = C / kKvTile;
+    constexpr int LPR = 32 / R, KPL = C / LPR;   // lanes a row, keys a lane
+    constexpr int kStride = C + 4;   // spreads a product's 8 keys x 4 row pairs over the banks
     constexpr bool F32 = sizeof(T) == 4;
-    extern __shared__ float xs[];    // [R][kStride]
+    __shared__ __align__(16) float xs_all[kScoreWarps][8 * NT * kStride];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    float* xs = xs_all[warp];
     const int bk = blockIdx.z, b = bk / a.Hkv, hk = bk - b * a.Hkv;
     const Kv4Seq s = seq_of(a, b);
     if (s.bad && a.bad && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(a.bad, s.bad);
     const int row0 = blockIdx.y * R, nrows = s.rows * a.group;   // real rows of this key head
-    int k0, k1;
-    kv4_chunk(a.g, s, C, blockIdx.x, &k0, &k1);
-    if (row0 >= nrows) return;
-    if (k0 >= k1) {
-        // a chunk of sinks that the sequence does not reach: empty, as the solver reads it
-        if (blockIdx.x < kv4_seq_chunks(a.g, s, C) && threadIdx.x < R && row0 + threadIdx.x < nrows) {
-            const size_t at = ((size_t)bk * a.g.L * a.group + row0 + threadIdx.x) * a.nchunk + blockIdx.x;
-            a.chunk_max[at] = -INFINITY;
-            a.chunk_n[at] = 0;
-        }
-        return;
-    }
+    const int nch = kv4_seq_chunks(a.g, s, C), run = kv4_run(nch, a.nsplit);
+    const int split = blockIdx.x * kScoreWarps + warp;
+    const int ch0 = split * run, ch1 = kv4_min(ch0 + run, nch);
+    if (row0 >= nrows || ch0 >= ch1) return;   // (the solver takes no more runs than hold a chunk)
 
     // ---- queries: lane (n = lane / 4, c = lane % 4) holds dimensions 32 w + 8 c + i of row n
     const int c = lane & 3;
     uint32_t qf[NT][G][4], ql[F32 ? NT : 1][G][4];   // B operands; float32 rows: high and low parts
-    float qz[NT][G][2], mul[NT][2], mul2[NT][2];     // of this lane's columns 2c, 2c + 1
-    int pos[NT][2];                                  // their positions (-1: no row)
+    uint32_t qz[NT][3];                              // sum q of group c in three parts
+    float mul[NT][2], mul2[NT][2];                   // of this lane's columns 2c, 2c + 1
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         const int r = row0 + nt * 8 + (lane >> 2);
-        const bool real = r < nrows;
+        const bool real = r < nrows && nt * 8 + (lane >> 2) < R;
         const int l = real ? r / a.group : 0, gi = real ? r - l * a.group : 0;
         const T* q = static_cast<const T*>(a.q) + (((size_t)b * a.Hkv * a.group + hk * a.group + gi) * a.g.L + l) * D;
         float x[G][8];
@@ -270,12 +281,14 @@ __global__ void __launch_bounds__(kKvThreads) kv4_scores_kernel(const Kv4Args a)
         }
         int e = 0;
         if (top > 0.f && fine) { frexpf(top, &e); e = 15 - e; }
+        const float fe1 = ldexpf(1.f, e / 2), fe2 = ldexpf(1.f, e - e / 2);
+        float zsum = 0.f;
 #pragma unroll
         for (int w = 0; w < G; ++w) {
             float sum = 0.f, hi[8], lo[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float y = ldexpf(x[w][i], e);
+                const float y = x[w][i] * fe1 * fe2;   // 2^e in two exact steps
                 hi[i] = __half2float(__float2half_rn(y));
                 lo[i] = y - hi[i];
                 sum += y;
@@ -293,47 +306,62 @@ __global__ void __launch_bounds__(kKvThreads) kv4_scores_kernel(const Kv4Args a)
             }
             sum += __shfl_xor_sync(kFull, sum, 1);
             sum += __shfl_xor_sync(kFull, sum, 2);
-            sum *= 5.9604644775390625e-08f;   // 2^-24, the codes' unit
-            qz[nt][w][0] = __shfl_sync(kFull, sum, 8 * c);
-            qz[nt][w][1] = __shfl_sync(kFull, sum, 8 * c + 4);
+            if (w == c) zsum = sum * 5.9604644775390625e-08f;   // 2^-24, the codes' unit
         }
+        qz[nt][0] = bf16_part(zsum);
+        qz[nt][1] = bf16_part(zsum);
+        qz[nt][2] = bf16_part(zsum);
         // x = cx 2^(24 - e) s: in two factors, either of which is in range
         const int e1 = (24 - e) / 2;
         // a row with a NaN or an infinity has NaN scores
         const float f1 = fine ? a.cx * ldexpf(1.f, e1) : nanf(""), f2 = ldexpf(1.f, 24 - e - e1);
-        const int p = real ? s.start + l : -1;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             mul[nt][k] = __shfl_sync(kFull, f1, 8 * c + 4 * k);
             mul2[nt][k] = __shfl_sync(kFull, f2, 8 * c + 4 * k);
-            pos[nt][k] = __shfl_sync(kFull, p, 8 * c + 4 * k);
         }
     }
-    // every row of this block is real and sees every key of the chunk
-    const int first = s.start + row0 / a.group, last_r = row0 + R - 1;
-    const bool whole = last_r < nrows && k1 - k0 == C && k1 - 1 <= first &&
-                       (!a.g.window || k1 <= a.g.sinks || k0 > s.start + last_r / a.group - a.g.window);
 
-    // ---- keys, U tiles of a warp at a time
+    // ---- keys, a chunk of U tiles at a time
     const int* table = a.table + (size_t)b * a.g.max_pages;
     const uint32_t* codes = reinterpret_cast<const uint32_t*>(a.k_codes);
     const uint32_t* meta = reinterpret_cast<const uint32_t*>(a.k_meta);
     const int key = lane >> 2;   // the lane's keys of a tile: key and key + 8
-#pragma unroll
-    for (int t0 = 0; t0 < kTiles; t0 += U) {
+    // the row that this lane looks through, in its lanes' part `sub`
+    const int lrow = lane / LPR, sub = lane % LPR;
+    const bool lreal = row0 + lrow < nrows;
+    const int lpos = lreal ? s.start + (row0 + lrow) / a.group : -1;
+    const size_t list = ((size_t)bk * a.g.L * a.group + row0 + lrow) * a.nsplit + split;
+    int2* out = a.cand + list * a.cap;
+    const int pos_first = s.start + row0 / a.group;
+    const int pos_last = s.start + (kv4_min(row0 + R, nrows) - 1) / a.group;
+    float m = -INFINITY;    // of the row, over the run so far
+    int n = 0;              // candidates of the row so far
+    bool nan = false;
+    // page of tile `lane` of a chunk (lanes below U), one chunk ahead of its loads
+    auto page_of = [&](int ch) {
+        int k0, k1, p = -1;
+        kv4_chunk(a.g, s, C, ch, &k0, &k1);
+        const int kb = k0 + (lane < U ? lane : 0) * kKvTile;
+        if (ch < ch1 && kb < k1) {
+            p = kv4_page(a.g, table, kb);
+            if (p < 0 && a.bad && lane < U) atomicOr(a.bad, kKvBadPage);
+        }
+        return p;
+    };
+    int pages = page_of(ch0);
+#pragma unroll 1
+    for (int ch = ch0; ch < ch1; ++ch) {
+        int k0, k1;
+        kv4_chunk(a.g, s, C, ch, &k0, &k1);
         uint32_t w[U][2][G], mt[U][2][G];
-        bool has[U];
+        unsigned has = 0;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int kb = k0 + ((t0 + u) * (kKvThreads / 32) + warp) * kKvTile;
-            int page = -1;
-            if (kb < k1) {
-                page = kv4_page(a.g, table, kb);
-                if (page < 0 && a.bad && lane == 0) atomicOr(a.bad, kKvBadPage);
-            }
-            has[u] = page >= 0;
-            if (has[u]) {
-                const size_t at = kv4_row(a.g, a.Hkv, page, hk, kb) + key;
+            const int page = __shfl_sync(kFull, pages, u);
+            if (page >= 0) {
+                has |= 1u << u;
+                const size_t at = kv4_row(a.g, a.Hkv, page, hk, k0 + u * kKvTile) + key;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     load_words<G>(codes + (at + 8 * h) * (D / 8) + c * G, w[u][h]);
@@ -346,14 +374,24 @@ __global__ void __launch_bounds__(kKvThreads) kv4_scores_kernel(const Kv4Args a)
                     for (int i = 0; i < G; ++i) { w[u][h][i] = 0u; mt[u][h][i] = 0u; }
             }
         }
+        pages = page_of(ch + 1);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int kt = ((t0 + u) * (kKvThreads / 32) + warp) * kKvTile;
             float acc[NT][4];
+            uint32_t mz[2];   // the pair of group c (lanes past the groups: zeros)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int h = 0; h < 2; ++h) {
+                mz[h] = c == 0 ? mt[u][h][0] : 0u;
+#pragma unroll
+                for (int i = 1; i < G; ++i) mz[h] = c == i ? mt[u][h][i] : mz[h];
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) acc[nt][k] = 0.f;
+                mma_16816_bf(acc[nt], mz[0], mz[1], mz[0], mz[1], qz[nt][0], qz[nt][1]);
+                mma_1688_bf(acc[nt], mz[0], mz[1], qz[nt][2]);
+            }
 #pragma unroll
             for (int i = 0; i < G; ++i) {
                 uint32_t w0 = w[u][0][i], w1 = w[u][1][i];
@@ -363,8 +401,7 @@ __global__ void __launch_bounds__(kKvThreads) kv4_scores_kernel(const Kv4Args a)
                 w0 >>= 8; w1 >>= 8;
                 av[4] = w0 & 0x000f000fu; av[5] = w1 & 0x000f000fu;
                 av[6] = w0 & 0x00f000f0u; av[7] = w1 & 0x00f000f0u;
-                const float s0 = bf16_lo(mt[u][0][i]), z0 = bf16_hi(mt[u][0][i]);
-                const float s1 = bf16_lo(mt[u][1][i]), z1 = bf16_hi(mt[u][1][i]);
+                const float s0 = bf16_lo(mt[u][0][i]), s1 = bf16_lo(mt[u][1][i]);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     float d[4] = {0.f, 0.f, 0.f, 0.f};
@@ -374,11 +411,10 @@ __global__ void __launch_bounds__(kKvThreads) kv4_scores_kernel(const Kv4Args a)
                         mma_16816(d, av[0], av[1], av[2], av[3], ql[nt][i][0], ql[nt][i][1]);
                         mma_16816(d, av[4], av[5], av[6], av[7], ql[nt][i][2], ql[nt][i][3]);
                     }
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        acc[nt][k] = fmaf(s0, d[k], fmaf(z0, qz[nt][i][k], acc[nt][k]));
-                        acc[nt][2 + k] = fmaf(s1, d[2 + k], fmaf(z1, qz[nt][i][k], acc[nt][2 + k]));
-                    }
+                    acc[nt][0] = fmaf(s0, d[0], acc[nt][0]);
+                    acc[nt][1] = fmaf(s0, d[1], acc[nt][1]);
+                    acc[nt][2] = fmaf(s1, d[2], acc[nt][2]);
+                    acc[nt][3] = fmaf(s1, d[3], acc[nt][3]);
                 }
             }
 #pragma unroll
@@ -386,73 +422,80 @@ __global__ void __launch_bounds__(kKvThreads) kv4_scores_kernel(const Kv4Args a)
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const int j = k0 + kt + key + 8 * h;
-                        float x = acc[nt][2 * h + k] * mul[nt][k] * mul2[nt][k];
-                        if (!whole || !has[u])
-                            x = (has[u] && j < k1 && kv4_sees(a.g, pos[nt][k], j)) ? x : -INFINITY;
-                        xs[(nt * 8 + 2 * c + k) * kStride + kt + key + 8 * h] = x;
-                    }
+                    for (int k = 0; k < 2; ++k)
+                        xs[(nt * 8 + 2 * c + k) * kStride + u * kKvTile + key + 8 * h] =
+                            acc[nt][2 * h + k] * mul[nt][k] * mul2[nt][k];
         }
-    }
-    __syncthreads();
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-
-    // ---- a warp per row: maximum, then the candidates in key order
-    const ChunkOut out{a.cand_x, a.cand_j, a.chunk_max, a.chunk_n};
+        __syncwarp();
+        // ---- the row's part of the chunk: keys (i * LPR + sub) * 4 + e
+        float v[KPL];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        const int r = nt * 8 + warp;
-        if (row0 + r >= nrows) break;
-        float v[C / 32];
-        float m = -INFINITY;
-        bool nan = false;
-#pragma unroll
-        for (int e = 0; e < C / 32; ++e) {
-            v[e] = xs[r * kStride + e * 32 + lane];
-            nan |= !(v[e] < INFINITY);
-            m = fmaxf(m, v[e]);
+        for (int i = 0; i < KPL / 4; ++i) {
+            const float4 f = *reinterpret_cast<const float4*>(xs + lrow * kStride + (i * LPR + sub) * 4);
+            v[4 * i] = f.x; v[4 * i + 1] = f.y; v[4 * i + 2] = f.z; v[4 * i + 3] = f.w;
         }
+        __syncwarp();
+        // not every row sees every key of the chunk: those it does not see leave as -inf
+        const bool whole = has == (1u << U) - 1u && k1 - k0 == C && k1 - 1 <= pos_first &&
+                           (!a.g.window || k1 <= a.g.sinks || k0 > pos_last - a.g.window);
+        if (!whole) {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-        nan = __any_sync(kFull, nan);
-        const size_t at = ((size_t)bk * a.g.L * a.group + row0 + r) * a.nchunk + blockIdx.x;
-    // the maximum itself is always kept: at |m| >= 2^24 it equals m - 1
-        const float lim = m - 1.f;
-        float* ox = out.x + at * C;
-        uint16_t* oj = out.j + at * C;
-        int n = 0;
-        if (!nan) {
-#pragma unroll
-            for (int e = 0; e < C / 32; ++e) {
-                const bool take = v[e] > lim || (v[e] == m && m > -INFINITY);
-                const unsigned mask = __ballot_sync(kFull, take);
-                if (take) {
-                    const int i = n + __popc(mask & ((1u << lane) - 1u));
-                    ox[i] = v[e];
-                    oj[i] = (uint16_t)(e * 32 + lane);
-                }
-                n += __popc(mask);
+            for (int i = 0; i < KPL; ++i) {
+                const int kk = ((i >> 2) * LPR + sub) * 4 + (i & 3);
+                const bool see = k0 + kk < k1 && (has >> (kk / kKvTile) & 1u) && kv4_sees(a.g, lpos, k0 + kk);
+                v[i] = see ? v[i] : -INFINITY;
             }
         }
-        if (lane == 0) {
-            out.m[at] = nan ? nanf("") : m;
-            out.n[at] = n;
+        float cm = v[0];
+#pragma unroll
+        for (int i = 1; i < KPL; ++i) cm = fmaxf(cm, v[i]);
+        bool odd = false;   // a NaN or +inf
+#pragma unroll
+        for (int i = 0; i < KPL; ++i) odd |= !(v[i] < INFINITY);
+        nan |= odd;
+#pragma unroll
+        for (int o = 1; o < LPR; o <<= 1) cm = fmaxf(cm, __shfl_xor_sync(kFull, cm, o));
+        m = fmaxf(m, cm);
+        // the maximum itself is always kept: at |m| >= 2^24 it equals m - 1
+        const float lim = m - 1.f;
+        unsigned take = 0;
+#pragma unroll
+        for (int i = 0; i < KPL; ++i) take |= (v[i] > lim || (v[i] == m && m > -INFINITY) ? 1u : 0u) << i;
+        if (!lreal) take = 0;
+        const int cnt = __popc(take);
+        int incl = cnt;
+#pragma unroll
+        for (int o = 1; o < LPR; o <<= 1) {
+            const int y = __shfl_up_sync(kFull, incl, o, LPR);
+            if (sub >= o) incl += y;
         }
+        int put = n + incl - cnt;
+        n += __shfl_sync(kFull, incl, LPR - 1, LPR);
+#pragma unroll
+        for (int i = 0; i < KPL; ++i)
+            if (take >> i & 1u)
+                out[put++] = make_int2(__float_as_int(v[i]), k0 + ((i >> 2) * LPR + sub) * 4 + (i & 3));
+    }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+#pragma unroll
+    for (int o = 1; o < LPR; o <<= 1) nan |= __shfl_xor_sync(kFull, (int)nan, o) != 0;
+    if (lreal && sub == 0) {
+        a.split_max[list] = nan ? nanf("") : m;
+        a.split_n[list] = n;
     }
 }
 
 // ------------------------------------------------------------------ solve and P.V
-// One CTA per query row.  The candidates above m - 1 (m the maximum over the chunks) are
-// gathered in key order into shared memory (kCap of them; a row with more goes over the
-// chunks' lists again in every pass), tau - m is found by Halley-bisection from the bracket
-// [-1, -n^(1-alpha)] (n the candidates' count: f <= 0 there since at most n keys weigh),
-// and O accumulates over the support, D/8 lanes per value row.  Scores are held relative
-// to m, so tau keeps its precision for scores of any size.  Every sum has a fixed order:
-// the result does not change from run to run.
+// One CTA per query row.  The runs' candidates are gathered in key order into shared memory,
+// those above m - 1 (m the maximum over the runs) kept, tau - m is found by Halley-bisection
+// from the bracket [-1, -n^(1-alpha)] (n the candidates' count: f <= 0 there since at most n
+// keys weigh), and O accumulates over the support, D/8 lanes per value row.  Scores are held
+// relative to m, so tau keeps its precision for scores of any size.  Every sum has a fixed
+// order: the result does not change from run to run.  A row with more than kCap candidates
+// even above m - 1 goes over the runs' lists again in every pass.
 constexpr int kSolveThreads = 128;
 constexpr int kSolveWarps = kSolveThreads / 32;
-constexpr int kCap = 2048;
+constexpr int kCap = 4096;
 constexpr float kKvFtol = 2e-7f, kKvStol = 6e-8f;   // to the rounding of the sums
 
 __device__ __forceinline__ float warp_sum(float x) {
@@ -482,6 +525,7 @@ __global__ void __launch_bounds__(kSolveThreads) kv4_solve_kernel(const Kv4Args 
     constexpr int G = D / kKvGroup, LPK = D / 8, KPW = 32 / LPK;
     __shared__ float ys[kCap];          // x - m of the candidates, then their weights
     __shared__ int js[kCap];            // their keys
+    __shared__ int off[kKvMaxSplit + 1];   // the runs' candidates before each run
     __shared__ float red[3][kSolveWarps];
     __shared__ int box[kSolveWarps];
     __shared__ float bc[2];
@@ -494,68 +538,118 @@ __global__ void __launch_bounds__(kSolveThreads) kv4_solve_kernel(const Kv4Args 
     const Kv4Seq s = seq_of(a, b);
     const size_t orow = ((size_t)b * a.Hkv * a.group + hk * a.group + gi) * a.g.L + l;
     T* o = static_cast<T*>(a.o) + orow * D;
-    const int C = a.chunk;
-    const int nch = l < s.rows ? kv4_seq_chunks(a.g, s, C) : 0;
-    const size_t at = ((size_t)bk * per + r) * a.nchunk;
-    const float* cm = a.chunk_max + at;
-    const int* cn = a.chunk_n + at;
-    const float* cx = a.cand_x + at * C;
-    const uint16_t* cj = a.cand_j + at * C;
+    int nrun = 0;
+    if (l < s.rows) {
+        const int nch = kv4_seq_chunks(a.g, s, a.chunk), run = kv4_run(nch, a.nsplit);
+        nrun = run > 0 ? (nch + run - 1) / run : 0;
+    }
+    const size_t at = ((size_t)bk * per + r) * a.nsplit;
+    const float* cm = a.split_max + at;
+    const int* cn = a.split_n + at;
+    const int2* cand = a.cand + at * a.cap;
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
-    // ---- row maximum
+    // ---- row maximum (every warp for itself), then the runs' offsets, a quarter each warp
     float m = -INFINITY;
     bool nan = false;
-    for (int i = tid; i < nch; i += kSolveThreads) {
+    for (int i = lane; i < nrun; i += 32) {
         const float x = cm[i];
         nan |= x != x;
         m = fmaxf(m, x);
     }
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, d));
-    if (lane == 0) red[0][warp] = m;
-    nan = __syncthreads_or(nan);
-#pragma unroll
-    for (int w = 0; w < kSolveWarps; ++w) m = fmaxf(m, red[0][w]);
+    nan = __any_sync(kFull, nan);
     if (nan || m == -INFINITY) {   // no key is seen: zeros
         const float v = nan ? nanf("") : 0.f;
         for (int i = tid; i < D; i += kSolveThreads) store_f(o, i, v);
         if (tid == 0 && a.tau) a.tau[orow] = v;
         return;
     }
-
-    // ---- candidates: each warp takes a run of chunks, counts, then places
-    const int c0 = (int)((long long)nch * warp / kSolveWarps), c1 = (int)((long long)nch * (warp + 1) / kSolveWarps);
-    int mine = 0;
-    for (int i = c0; i < c1; ++i) {
-        if (!(cm[i] - m > -1.f)) continue;
-        const int n = cn[i];
-        for (int e = lane; e < n; e += 32) mine += cx[(size_t)i * C + e] - m > -1.f;
+    // (warps share the runs out here, and again when there are more candidates than fit)
+    const int c0 = (int)((long long)nrun * warp / kSolveWarps), c1 = (int)((long long)nrun * (warp + 1) / kSolveWarps);
+    int sum = 0;
+    for (int i0 = c0; i0 < c1; i0 += 32) {
+        const int i = i0 + lane;
+        const int n = i < c1 && cm[i] - m > -1.f ? cn[i] : 0;
+        int incl = n;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int y = __shfl_up_sync(kFull, incl, d);
+            if (lane >= d) incl += y;
+        }
+        if (i < c1) off[i] = sum + incl - n;
+        sum += __shfl_sync(kFull, incl, 31);
     }
-    mine = __reduce_add_sync(kFull, mine);
-    int total;
-    int put = warps_before(mine, box, &total);
-    const bool fits = total <= kCap;
-    if (fits) {
+    int raw;
+    const int before = warps_before(sum, box, &raw);
+    for (int i = c0 + lane; i < c1; i += 32) off[i] += before;
+    if (tid == 0) off[nrun] = raw;
+    __syncthreads();
+
+    // ---- candidates: each warp holds a run [e0, e0 + mine) of the arrays
+    const bool direct = raw <= kCap;
+    bool fits = true;
+    int e0, mine = 0, total;
+    if (direct) {
+        e0 = (int)((long long)raw * warp / kSolveWarps);
+        const int e1 = (int)((long long)raw * (warp + 1) / kSolveWarps);
+        int i = 0;   // the run that holds entry e0 (by halving), then forward
+        for (int step = kKvMaxSplit; step > 0; step >>= 1)
+            if (i + step < nrun && off[i + step] <= e0) i += step;
+        constexpr int U = 4;
+        for (int base = e0; base < e1; base += 32 * U) {
+            int2 c[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int e = base + u * 32 + lane;
+                c[u] = make_int2(0, -1);
+                if (e < e1) {
+                    while (off[i + 1] <= e) ++i;
+                    c[u] = cand[(size_t)i * a.cap + (e - off[i])];
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const float y = __int_as_float(c[u].x) - m;
+                const bool take = c[u].y >= 0 && y > -1.f;
+                const unsigned mask = __ballot_sync(kFull, take);
+                if (take) {
+                    const int p = e0 + mine + __popc(mask & ((1u << lane) - 1u));
+                    ys[p] = y;
+                    js[p] = c[u].y;
+                }
+                mine += __popc(mask);
+            }
+        }
+        warps_before(mine, box, &total);
+    } else {
         for (int i = c0; i < c1; ++i) {
-            if (!(cm[i] - m > -1.f)) continue;
-            const int n = cn[i];
-            int k0, k1;
-            kv4_chunk(a.g, s, C, i, &k0, &k1);
-            for (int e0 = 0; e0 < n; e0 += 32) {
-                const int e = e0 + lane;
-                const float y = e < n ? cx[(size_t)i * C + e] - m : -2.f;
-                const unsigned mask = __ballot_sync(kFull, y > -1.f);
-                if (y > -1.f) {
+            const int n = off[i + 1] - off[i];
+            for (int e = lane; e < n; e += 32) mine += __int_as_float(cand[(size_t)i * a.cap + e].x) - m > -1.f;
+        }
+        mine = __reduce_add_sync(kFull, mine);
+        e0 = warps_before(mine, box, &total);
+        fits = total <= kCap;
+        int put = e0;
+        for (int i = c0; fits && i < c1; ++i) {
+            const int n = off[i + 1] - off[i];
+            for (int b0 = 0; b0 < n; b0 += 32) {
+                const int e = b0 + lane;
+                const int2 c = e < n ? cand[(size_t)i * a.cap + e] : make_int2(0, -1);
+                const float y = __int_as_float(c.x) - m;
+                const bool take = c.y >= 0 && y > -1.f;
+                const unsigned mask = __ballot_sync(kFull, take);
+                if (take) {
                     const int p = put + __popc(mask & ((1u << lane) - 1u));
                     ys[p] = y;
-                    js[p] = k0 + cj[(size_t)i * C + e];
+                    js[p] = c.y;
                 }
                 put += __popc(mask);
             }
         }
     }
-    __syncthreads();
+    __syncwarp();
 
     // ---- tau - m
     const float gamma = a.gamma;
@@ -573,12 +667,11 @@ __global__ void __launch_bounds__(kSolveThreads) kv4_solve_kernel(const Kv4Args 
             F0 += t0; F1 += t1; F2 += t2;
         };
         if (fits) {
-            for (int i = tid; i < total; i += kSolveThreads) add(ys[i]);
+            for (int i = lane; i < mine; i += 32) add(ys[e0 + i]);
         } else {
             for (int i = c0; i < c1; ++i) {
-                if (!(cm[i] - m > -1.f)) continue;
-                const int n = cn[i];
-                for (int e = lane; e < n; e += 32) add(cx[(size_t)i * C + e] - m);
+                const int n = off[i + 1] - off[i];
+                for (int e = lane; e < n; e += 32) add(__int_as_float(cand[(size_t)i * a.cap + e].x) - m);
             }
         }
         F0 = warp_sum(F0); F1 = warp_sum(F1); F2 = warp_sum(F2);
@@ -620,14 +713,12 @@ __global__ void __launch_bounds__(kSolveThreads) kv4_solve_kernel(const Kv4Args 
         for (int i = 0; i < 8; ++i) acc[i] = fmaf(ps, (float)((w >> (4 * i)) & 15u), acc[i]);
     };
     if (fits) {
-        // the support in key order, over the same arrays: each warp compacts its run, then
-        // the runs are closed up
-        const int e0 = (int)((long long)total * warp / kSolveWarps), e1 = (int)((long long)total * (warp + 1) / kSolveWarps);
+        // the support in key order, over the same arrays: each warp compacts its own run
         int n = 0;
-        for (int base = e0; base < e1; base += 32) {
+        for (int base = 0; base < mine; base += 32) {
             const int e = base + lane;
-            const float p = e < e1 ? entmax_p<GM>(ys[e] - sv.tau, gamma) : 0.f;
-            const int j = e < e1 ? js[e] : 0;
+            const float p = e < mine ? entmax_p<GM>(ys[e0 + e] - sv.tau, gamma) : 0.f;
+            const int j = e < mine ? js[e0 + e] : 0;
             const unsigned mask = __ballot_sync(kFull, p > 0.f);
             __syncwarp();
             if (p > 0.f) {
@@ -638,21 +729,25 @@ __global__ void __launch_bounds__(kSolveThreads) kv4_solve_kernel(const Kv4Args 
             n += __popc(mask);
             __syncwarp();
         }
+        if (lane == 0) red[0][warp] = __int_as_float(e0);
         int sup;
         warps_before(n, box, &sup);
-        __syncthreads();
         // entry i of the support: in the run of the warp whose counts it falls into
-        int ends[kSolveWarps];
+        int ends[kSolveWarps], from[kSolveWarps];
 #pragma unroll
-        for (int w = 0, sum = 0; w < kSolveWarps; ++w) { sum += box[w]; ends[w] = sum; }
+        for (int w = 0, sum = 0; w < kSolveWarps; ++w) {
+            from[w] = __float_as_int(red[0][w]) - sum;
+            sum += box[w];
+            ends[w] = sum;
+        }
         auto where = [&](int i) {
-            int w = 0, before = 0;
+            int f = from[0];
 #pragma unroll
             for (int k = 0; k + 1 < kSolveWarps; ++k)
-                if (i >= ends[k]) { w = k + 1; before = ends[k]; }
-            return (int)((long long)total * w / kSolveWarps) + i - before;
+                if (i >= ends[k]) f = from[k + 1];
+            return f + i;
         };
-        constexpr int U = 4, STEP = kSolveWarps * KPW;
+        constexpr int U = 8, STEP = kSolveWarps * KPW;
         for (int i0 = warp * KPW + slot; i0 < sup; i0 += U * STEP) {
             float p[U];
             uint32_t w[U], mt[U];
@@ -672,15 +767,13 @@ __global__ void __launch_bounds__(kSolveThreads) kv4_solve_kernel(const Kv4Args 
         }
     } else {
         for (int i = c0; i < c1; ++i) {
-            if (!(cm[i] - m > sv.tau)) continue;
-            const int n = cn[i];
-            int k0, k1;
-            kv4_chunk(a.g, s, C, i, &k0, &k1);
+            const int n = off[i + 1] - off[i];
             for (int e = slot; e < n; e += KPW) {
-                const float p = entmax_p<GM>(cx[(size_t)i * C + e] - m - sv.tau, gamma);
+                const int2 c = cand[(size_t)i * a.cap + e];
+                const float p = entmax_p<GM>(__int_as_float(c.x) - m - sv.tau, gamma);
                 if (!(p > 0.f)) continue;
                 uint32_t w, mt;
-                fetch(k0 + cj[(size_t)i * C + e], w, mt);
+                fetch(c.y, w, mt);
                 weigh(p, w, mt);
             }
         }
@@ -715,26 +808,22 @@ cudaError_t write_or_read(const Kv4Args& a, bool write, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-template <typename T, int D, int NT>
+template <typename T, int D, int R>
 cudaError_t launch_scores(const Kv4Args& a, cudaStream_t s) {
     const int rows = a.g.L * a.group;
-    const size_t sm = (size_t)8 * NT * (kv4_chunk_keys(NT) + 4) * sizeof(float);
-    auto kern = kv4_scores_kernel<T, D, NT>;
-    if (sm > 48 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
-        if (e != cudaSuccess) return e;
-    }
-    kern<<<dim3(a.nchunk, (rows + 8 * NT - 1) / (8 * NT), a.g.B * a.Hkv), kKvThreads, sm, s>>>(a);
+    const dim3 grid((a.nsplit + kScoreWarps - 1) / kScoreWarps, (rows + R - 1) / R, a.g.B * a.Hkv);
+    kv4_scores_kernel<T, D, R><<<grid, kScoreThreads, 0, s>>>(a);
     return cudaGetLastError();
 }
 
 template <typename T, int D>
 cudaError_t attn(const Kv4Args& a, int gm, cudaStream_t s) {
     cudaError_t e = cudaSuccess;
-    if (a.nchunk > 0) switch (a.ntile) {   // (a call that covers no token: zeros only)
-        case 1: e = launch_scores<T, D, 1>(a, s); break;
-        case 2: e = launch_scores<T, D, 2>(a, s); break;
-        default: e = launch_scores<T, D, 4>(a, s); break;
+    if (a.nchunk > 0) switch (a.block) {   // (a call that covers no token: zeros only)
+        case 4: e = launch_scores<T, D, 4>(a, s); break;
+        case 8: e = launch_scores<T, D, 8>(a, s); break;
+        case 16: e = launch_scores<T, D, 16>(a, s); break;
+        default: e = launch_scores<T, D, 32>(a, s); break;
     }
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};

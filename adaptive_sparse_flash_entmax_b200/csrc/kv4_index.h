@@ -118,6 +118,10 @@ ENT_HD void kv4_chunk(const Kv4Geom& g, const Kv4Seq& s, int C, int c, int* k0, 
     }
 }
 
+// The chunks of a sequence are dealt to `nsplit` runs of equal length: run i holds chunks
+// [i * kv4_run, (i + 1) * kv4_run) below kv4_seq_chunks.
+ENT_HD int kv4_run(int seq_chunks, int nsplit) { return (seq_chunks + nsplit - 1) / nsplit; }
+
 // Whether the row at position pos sees key j.
 ENT_HD bool kv4_sees(const Kv4Geom& g, int pos, int j) {
     return j <= pos && (!g.window || pos - j < g.window || j < g.sinks);

@@ -12,6 +12,7 @@ position of row 0 (the tokens cached before), ``new_lens`` int32 [B] the rows th
 """
 from __future__ import annotations
 
+import functools
 from typing import NamedTuple
 
 import torch
@@ -75,6 +76,10 @@ def _check_seqs(block_table, start, new_lens, bad, B, device):
             bad.data_ptr() if bad is not None else None, block_table.shape[1])
 
 
+# sizes alone go in: a decoder asks with the same ones at every step
+_workspace_size = functools.lru_cache(maxsize=256)(lambda *sizes: capi.ent_attn_kv4_workspace_size(*sizes))
+
+
 def _check_rows4(*ts):
     t0 = ts[0]
     if t0.dim() != 4:
@@ -91,7 +96,7 @@ def _check_rows4(*ts):
 
 def _call(fn, device, *args):
     """fn(*args, stream) with the tensors' device current."""
-    if device.index == torch.cuda.current_device():
+    if device.index == torch._C._cuda_getDevice():
         st = fn(*args, _stream_handle(device))
     else:
         with torch.cuda.device(device):
@@ -144,8 +149,8 @@ def kv4_workspace(q, cache, block_table, *, window: int | None = None, sinks: in
     """A workspace for ``entmax_attn_kv4`` of these arguments; it serves one call at a time."""
     B, Hq, L, d = q.shape
     cap = block_table.shape[1] * cache[0].shape[2]
-    n = capi.ent_attn_kv4_workspace_size(B, Hq, cache[0].shape[1], L, d, _DTYPES[q.dtype],
-                                         cap if max_len is None else max_len, window or 0, sinks)
+    n = _workspace_size(B, Hq, cache[0].shape[1], L, d, _DTYPES[q.dtype], cap if max_len is None else max_len,
+                        window or 0, sinks)
     return torch.empty(max(n, 256), dtype=torch.uint8, device=q.device)
 
 
@@ -182,7 +187,7 @@ def entmax_attn_kv4(q, cache, block_table, start, alpha: float = 1.5, *, new_len
     if tau is not None and (tau.dtype != torch.float32 or tau.shape != (B, Hq, L) or tau.device != device
                             or not tau.is_contiguous()):
         raise ValueError("tau must be a contiguous float32 tensor [B, Hq, L] on the device of q")
-    need = capi.ent_attn_kv4_workspace_size(B, Hq, heads, L, d, dt, max_len, window, sinks)
+    need = _workspace_size(B, Hq, heads, L, d, dt, max_len, window, sinks)
     if ws is None or ws.numel() < need:
         ws = torch.empty(max(need, 256), dtype=torch.uint8, device=device)
     elif ws.dtype != torch.uint8 or ws.device != device or not ws.is_contiguous():
