@@ -708,14 +708,15 @@ ent_status check_kv4(ent::Kv4Args& a, const void* kc, const void* km, const void
         return fail(ENT_EUNSUPPORTED, "head dim d=%d (supported: 32, 64, 128)", d);
     if (page < ent::kKvTile || (page & (page - 1)) != 0)
         return fail(ENT_EINVAL, "page of %d tokens (a power of two of at least %d)", page, ent::kKvTile);
-    if (pages < 0 || max_pages < 0) return fail(ENT_EINVAL, "negative size (pages=%d max_pages=%d)", pages, max_pages);
+    if (max_pages < 0) return fail(ENT_EINVAL, "negative size (max_pages=%d)", max_pages);
     if ((long long)B * Hkv > 65535) return fail(ENT_EUNSUPPORTED, "B*Hkv=%lld exceeds 65535", (long long)B * Hkv);
     if ((long long)max_pages * page > 1ll << 30)   // positions and chunk ends stay clear of 31 bits
         return fail(ENT_EUNSUPPORTED, "max_pages * page = %lld tokens exceed 2^30", (long long)max_pages * page);
     if ((long long)B * Hkv * L > 0x7fffffffll) return fail(ENT_EUNSUPPORTED, "B*Hkv*L exceeds 31 bits");
     if (B > 0 && L > 0) {
         if ((!table && max_pages > 0) || !start) return fail(ENT_EINVAL, "null block_table/start pointer");
-        if (pages > 0 && (!kc || !km || !vc || !vm)) return fail(ENT_EINVAL, "null cache pointer");
+        if (pages < 1) return fail(ENT_EINVAL, "a pool without pages");
+        if (!kc || !km || !vc || !vm) return fail(ENT_EINVAL, "null cache pointer");
         if (!aligned16(kc) || !aligned16(km) || !aligned16(vc) || !aligned16(vm))
             return fail(ENT_EINVAL, "cache arrays must be 16-byte aligned");
     }

@@ -168,8 +168,8 @@ __global__ void __launch_bounds__(kKvThreads) kv4_read_kernel(const Kv4Args a) {
 }
 
 // ------------------------------------------------------------------ scores
-// A warp per (run of chunks of C keys, block of R rows, sequence and key head): four warps a
-// CTA that share nothing.  The rows are the new tokens' queries of all heads that share the
+// A warp per (run of chunks of C keys, block of R rows, sequence and key head); the eight warps
+// of a CTA share nothing but the rows' maxima so far.  The rows are the new tokens' queries of all heads that share the
 // key head, row = l * group + head of the group.  Keys are the M = 16 rows of an m16n8k16
 // product and the queries its 8 columns; the contraction index is permuted so that a lane's
 // four A registers are its own words of two keys, masked: a nibble at bits 0-3 of a half is
@@ -184,18 +184,26 @@ __global__ void __launch_bounds__(kKvThreads) kv4_read_kernel(const Kv4Args a) {
 // [2^14, 2^15): exact for bf16 values down to 2^-31 of the largest, below which the
 // rounding is 2^-39 of it; a float32 row is the sum of two such halves (22 bits).
 // The scores of a chunk pass through the warp's shared memory (queries by keys), where 32/R
-// lanes a row take their maximum and the candidates above the run's maximum so far - 1.
+// lanes a row take their maximum and the candidates above the CTA's maximum so far - 1 (which
+// of the warps got how far does not matter: the solver drops what the final maximum rules out).
+// c = A B (+ c); the first form takes no accumulator, so that none has to be cleared
+__device__ __forceinline__ void mma_16816_0(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                            uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                           uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void mma_16816_bf(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                             uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+__device__ __forceinline__ void mma_16816_bf_0(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 __device__ __forceinline__ void mma_1688_bf(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
     asm("mma.sync.aligned.m16n8k8.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%0,%1,%2,%3};"
@@ -206,6 +214,12 @@ __device__ __forceinline__ void mma_1688_bf(float (&c)[4], uint32_t a0, uint32_t
 __device__ __forceinline__ uint32_t pack_half(float a, float b) {
     const __half2 h = __floats2half2_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&h);
+}
+// the larger, or NaN where either is
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
 }
 // x rounded to bf16, in the upper half of a word; what is left stays in x
 __device__ __forceinline__ uint32_t bf16_part(float& x) {
@@ -228,17 +242,18 @@ __device__ __forceinline__ void load_words(const uint32_t* p, uint32_t (&w)[G]) 
     }
 }
 
-constexpr int kScoreThreads = 128;
+constexpr int kScoreThreads = 256;
 constexpr int kScoreWarps = kScoreThreads / 32;
 
 // R: rows of a block (4, 8, 16 or 32), in NT products of 8 columns.
 template <typename T, int D, int R>
-__global__ void __launch_bounds__(kScoreThreads, R <= 8 ? 4 : R <= 16 ? 3 : 2) kv4_scores_kernel(const Kv4Args a) {
+__global__ void __launch_bounds__(kScoreThreads, R <= 8 ? 2 : 1) kv4_scores_kernel(const Kv4Args a) {
     constexpr int G = D / kKvGroup, NT = R <= 8 ? 1 : R / 8, C = kv4_chunk_keys(R), U = C / kKvTile;
     constexpr int LPR = 32 / R, KPL = C / LPR;   // lanes a row, keys a lane
     constexpr int kStride = C + 4;   // spreads a product's 8 keys x 4 row pairs over the banks
     constexpr bool F32 = sizeof(T) == 4;
     __shared__ __align__(16) float xs_all[kScoreWarps][8 * NT * kStride];
+    __shared__ float row_max[R];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     float* xs = xs_all[warp];
     const int bk = blockIdx.z, b = bk / a.Hkv, hk = bk - b * a.Hkv;
@@ -248,13 +263,17 @@ __global__ void __launch_bounds__(kScoreThreads, R <= 8 ? 4 : R <= 16 ? 3 : 2) k
     const int nch = kv4_seq_chunks(a.g, s, C), run = kv4_run(nch, a.nsplit);
     const int split = blockIdx.x * kScoreWarps + warp;
     const int ch0 = split * run, ch1 = kv4_min(ch0 + run, nch);
+    if (threadIdx.x < R) row_max[threadIdx.x] = -INFINITY;
+    __syncthreads();
     if (row0 >= nrows || ch0 >= ch1) return;   // (the solver takes no more runs than hold a chunk)
 
     // ---- queries: lane (n = lane / 4, c = lane % 4) holds dimensions 32 w + 8 c + i of row n
     const int c = lane & 3;
     uint32_t qf[NT][G][4], ql[F32 ? NT : 1][G][4];   // B operands; float32 rows: high and low parts
     uint32_t qz[NT][3];                              // sum q of group c in three parts
-    float mul[NT][2], mul2[NT][2];                   // of this lane's columns 2c, 2c + 1
+    // the row that this lane looks through, in its lanes' part `sub`, and its factors
+    const int lrow = lane / LPR, sub = lane % LPR;
+    float mul = 0.f, mul2 = 0.f;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         const int r = row0 + nt * 8 + (lane >> 2);
@@ -315,20 +334,13 @@ __global__ void __launch_bounds__(kScoreThreads, R <= 8 ? 4 : R <= 16 ? 3 : 2) k
         const int e1 = (24 - e) / 2;
         // a row with a NaN or an infinity has NaN scores
         const float f1 = fine ? a.cx * ldexpf(1.f, e1) : nanf(""), f2 = ldexpf(1.f, 24 - e - e1);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            mul[nt][k] = __shfl_sync(kFull, f1, 8 * c + 4 * k);
-            mul2[nt][k] = __shfl_sync(kFull, f2, 8 * c + 4 * k);
-        }
+        const float g1 = __shfl_sync(kFull, f1, 4 * (lrow & 7)), g2 = __shfl_sync(kFull, f2, 4 * (lrow & 7));
+        if (lrow >> 3 == nt) { mul = g1; mul2 = g2; }
     }
 
     // ---- keys, a chunk of U tiles at a time
     const int* table = a.table + (size_t)b * a.g.max_pages;
-    const uint32_t* codes = reinterpret_cast<const uint32_t*>(a.k_codes);
-    const uint32_t* meta = reinterpret_cast<const uint32_t*>(a.k_meta);
     const int key = lane >> 2;   // the lane's keys of a tile: key and key + 8
-    // the row that this lane looks through, in its lanes' part `sub`
-    const int lrow = lane / LPR, sub = lane % LPR;
     const bool lreal = row0 + lrow < nrows;
     const int lpos = lreal ? s.start + (row0 + lrow) / a.group : -1;
     const size_t list = ((size_t)bk * a.g.L * a.group + row0 + lrow) * a.nsplit + split;
@@ -337,41 +349,48 @@ __global__ void __launch_bounds__(kScoreThreads, R <= 8 ? 4 : R <= 16 ? 3 : 2) k
     const int pos_last = s.start + (kv4_min(row0 + R, nrows) - 1) / a.group;
     float m = -INFINITY;    // of the row, over the run so far
     int n = 0;              // candidates of the row so far
-    bool nan = false;
+    // chunk ch holds keys k0 .. k1-1 (kv4_chunk, with what does not change taken out)
+    const int ns = kv4_sink_chunks(a.g, C), sink_end = kv4_min(kv4_sink_end(a.g), s.end);
+    const int base = kv4_base(a.g, s.start) - ns * C;
+    auto first_key = [&](int ch) { return ch * C + (ch < ns ? 0 : base); };
+    auto end_key = [&](int ch, int k0) { return kv4_min(k0 + C, ch < ns ? sink_end : s.end); };
     // page of tile `lane` of a chunk (lanes below U), one chunk ahead of its loads
     auto page_of = [&](int ch) {
-        int k0, k1, p = -1;
-        kv4_chunk(a.g, s, C, ch, &k0, &k1);
-        const int kb = k0 + (lane < U ? lane : 0) * kKvTile;
-        if (ch < ch1 && kb < k1) {
-            p = kv4_page(a.g, table, kb);
-            if (p < 0 && a.bad && lane < U) atomicOr(a.bad, kKvBadPage);
+        int p = -1;
+        if (ch < ch1 && lane < U) {
+            const int k0 = first_key(ch), kb = k0 + lane * kKvTile;
+            if (kb < end_key(ch, k0)) {
+                p = kv4_page(a.g, table, kb);
+                if (p < 0 && a.bad) atomicOr(a.bad, kKvBadPage);
+            }
         }
         return p;
     };
+    // bytes: of a token, of a page of all heads, and the lane's place in this head's page
+    constexpr int kTokenB = D / 2, kMetaB = 4 * G;
+    const size_t page_b = (size_t)a.Hkv << a.g.page_shift;
+    const int mask = (1 << a.g.page_shift) - 1;
+    const char* lane_codes = reinterpret_cast<const char*>(a.k_codes) +
+                             (((size_t)hk << a.g.page_shift) + key) * kTokenB + c * 4 * G;
+    const char* lane_meta = reinterpret_cast<const char*>(a.k_meta) +
+                            (((size_t)hk << a.g.page_shift) + key) * kMetaB;
     int pages = page_of(ch0);
 #pragma unroll 1
     for (int ch = ch0; ch < ch1; ++ch) {
-        int k0, k1;
-        kv4_chunk(a.g, s, C, ch, &k0, &k1);
+        const int k0 = first_key(ch), k1 = end_key(ch, k0);
         uint32_t w[U][2][G], mt[U][2][G];
-        unsigned has = 0;
+        const unsigned has = __ballot_sync(kFull, pages >= 0);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int page = __shfl_sync(kFull, pages, u);
-            if (page >= 0) {
-                has |= 1u << u;
-                const size_t at = kv4_row(a.g, a.Hkv, page, hk, k0 + u * kKvTile) + key;
+            // a tile that is not there reads the pool's first page instead, and no row sees it
+            const int page = max(__shfl_sync(kFull, pages, u), 0);
+            const size_t row = page * page_b + ((k0 + u * kKvTile) & mask);
+            const char* pc = lane_codes + row * kTokenB;
+            const char* pm = lane_meta + row * kMetaB;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    load_words<G>(codes + (at + 8 * h) * (D / 8) + c * G, w[u][h]);
-                    load_words<G>(meta + (at + 8 * h) * G, mt[u][h]);
-                }
-            } else {
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int i = 0; i < G; ++i) { w[u][h][i] = 0u; mt[u][h][i] = 0u; }
+            for (int h = 0; h < 2; ++h) {
+                load_words<G>(reinterpret_cast<const uint32_t*>(pc + 8 * h * kTokenB), w[u][h]);
+                load_words<G>(reinterpret_cast<const uint32_t*>(pm + 8 * h * kMetaB), mt[u][h]);
             }
         }
         pages = page_of(ch + 1);
@@ -387,9 +406,7 @@ __global__ void __launch_bounds__(kScoreThreads, R <= 8 ? 4 : R <= 16 ? 3 : 2) k
             }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) acc[nt][k] = 0.f;
-                mma_16816_bf(acc[nt], mz[0], mz[1], mz[0], mz[1], qz[nt][0], qz[nt][1]);
+                mma_16816_bf_0(acc[nt], mz[0], mz[1], mz[0], mz[1], qz[nt][0], qz[nt][1]);
                 mma_1688_bf(acc[nt], mz[0], mz[1], qz[nt][2]);
             }
 #pragma unroll
@@ -404,8 +421,8 @@ __global__ void __launch_bounds__(kScoreThreads, R <= 8 ? 4 : R <= 16 ? 3 : 2) k
                 const float s0 = bf16_lo(mt[u][0][i]), s1 = bf16_lo(mt[u][1][i]);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    float d[4] = {0.f, 0.f, 0.f, 0.f};
-                    mma_16816(d, av[0], av[1], av[2], av[3], qf[nt][i][0], qf[nt][i][1]);
+                    float d[4];
+                    mma_16816_0(d, av[0], av[1], av[2], av[3], qf[nt][i][0], qf[nt][i][1]);
                     mma_16816(d, av[4], av[5], av[6], av[7], qf[nt][i][2], qf[nt][i][3]);
                     if constexpr (F32) {
                         mma_16816(d, av[0], av[1], av[2], av[3], ql[nt][i][0], ql[nt][i][1]);
@@ -423,8 +440,7 @@ __global__ void __launch_bounds__(kScoreThreads, R <= 8 ? 4 : R <= 16 ? 3 : 2) k
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int k = 0; k < 2; ++k)
-                        xs[(nt * 8 + 2 * c + k) * kStride + u * kKvTile + key + 8 * h] =
-                            acc[nt][2 * h + k] * mul[nt][k] * mul2[nt][k];
+                        xs[(nt * 8 + 2 * c + k) * kStride + u * kKvTile + key + 8 * h] = acc[nt][2 * h + k];
         }
         __syncwarp();
         // ---- the row's part of the chunk: keys (i * LPR + sub) * 4 + e
@@ -432,7 +448,8 @@ __global__ void __launch_bounds__(kScoreThreads, R <= 8 ? 4 : R <= 16 ? 3 : 2) k
 #pragma unroll
         for (int i = 0; i < KPL / 4; ++i) {
             const float4 f = *reinterpret_cast<const float4*>(xs + lrow * kStride + (i * LPR + sub) * 4);
-            v[4 * i] = f.x; v[4 * i + 1] = f.y; v[4 * i + 2] = f.z; v[4 * i + 3] = f.w;
+            v[4 * i] = f.x * mul * mul2; v[4 * i + 1] = f.y * mul * mul2;
+            v[4 * i + 2] = f.z * mul * mul2; v[4 * i + 3] = f.w * mul * mul2;
         }
         __syncwarp();
         // not every row sees every key of the chunk: those it does not see leave as -inf
@@ -446,21 +463,21 @@ __global__ void __launch_bounds__(kScoreThreads, R <= 8 ? 4 : R <= 16 ? 3 : 2) k
                 v[i] = see ? v[i] : -INFINITY;
             }
         }
-        float cm = v[0];
+        // a NaN passes through every maximum; +inf is caught at the end.  (A store that loses to
+        // another warp's costs a weaker filter, no more.)
+        m = max_nan(m, *const_cast<volatile float*>(&row_max[lrow]));
 #pragma unroll
-        for (int i = 1; i < KPL; ++i) cm = fmaxf(cm, v[i]);
-        bool odd = false;   // a NaN or +inf
+        for (int i = 0; i < KPL; ++i) m = max_nan(m, v[i]);
 #pragma unroll
-        for (int i = 0; i < KPL; ++i) odd |= !(v[i] < INFINITY);
-        nan |= odd;
-#pragma unroll
-        for (int o = 1; o < LPR; o <<= 1) cm = fmaxf(cm, __shfl_xor_sync(kFull, cm, o));
-        m = fmaxf(m, cm);
-        // the maximum itself is always kept: at |m| >= 2^24 it equals m - 1
-        const float lim = m - 1.f;
+        for (int o = 1; o < LPR; o <<= 1) m = max_nan(m, __shfl_xor_sync(kFull, m, o));
+        if (sub == 0) *const_cast<volatile float*>(&row_max[lrow]) = m;
+        // above m - 1, and the maximum itself: where |m| >= 2^24 makes them equal, the limit is
+        // the next float below m (m = -inf or NaN: it is NaN, and nothing is above)
+        float lim = m - 1.f;
+        if (!(lim < m)) lim = __int_as_float(__float_as_int(m) + (m > 0.f ? -1 : 1));
         unsigned take = 0;
 #pragma unroll
-        for (int i = 0; i < KPL; ++i) take |= (v[i] > lim || (v[i] == m && m > -INFINITY) ? 1u : 0u) << i;
+        for (int i = 0; i < KPL; ++i) take |= (v[i] > lim ? 1u : 0u) << i;
         if (!lreal) take = 0;
         const int cnt = __popc(take);
         int incl = cnt;
@@ -477,10 +494,8 @@ __global__ void __launch_bounds__(kScoreThreads, R <= 8 ? 4 : R <= 16 ? 3 : 2) k
                 out[put++] = make_int2(__float_as_int(v[i]), k0 + ((i >> 2) * LPR + sub) * 4 + (i & 3));
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-#pragma unroll
-    for (int o = 1; o < LPR; o <<= 1) nan |= __shfl_xor_sync(kFull, (int)nan, o) != 0;
     if (lreal && sub == 0) {
-        a.split_max[list] = nan ? nanf("") : m;
+        a.split_max[list] = m < INFINITY ? m : nanf("");
         a.split_n[list] = n;
     }
 }
@@ -527,7 +542,7 @@ __global__ void __launch_bounds__(kSolveThreads) kv4_solve_kernel(const Kv4Args 
     __shared__ int js[kCap];            // their keys
     __shared__ int off[kKvMaxSplit + 1];   // the runs' candidates before each run
     __shared__ float red[3][kSolveWarps];
-    __shared__ int box[kSolveWarps];
+    __shared__ int box[kSolveWarps], box2[kSolveWarps];
     __shared__ float bc[2];
     __shared__ float part[kSolveWarps][D];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -622,34 +637,64 @@ __global__ void __launch_bounds__(kSolveThreads) kv4_solve_kernel(const Kv4Args 
                 mine += __popc(mask);
             }
         }
-        warps_before(mine, box, &total);
     } else {
+        // each warp closes up its own lists in the workspace, so that what follows does not
+        // depend on what the scores kernel left in them
         for (int i = c0; i < c1; ++i) {
+            int2* list = a.cand + (at + i) * a.cap;
             const int n = off[i + 1] - off[i];
-            for (int e = lane; e < n; e += 32) mine += __int_as_float(cand[(size_t)i * a.cap + e].x) - m > -1.f;
+            int kept = 0;
+            for (int b0 = 0; b0 < n; b0 += 32) {
+                const int e = b0 + lane;
+                const int2 c = e < n ? list[e] : make_int2(0, -1);
+                const bool take = c.y >= 0 && __int_as_float(c.x) - m > -1.f;
+                const unsigned mask = __ballot_sync(kFull, take);
+                if (take) list[kept + __popc(mask & ((1u << lane) - 1u))] = c;
+                kept += __popc(mask);
+                __syncwarp();
+            }
+            if (lane == 0) a.split_n[at + i] = kept;
+            mine += kept;
         }
-        mine = __reduce_add_sync(kFull, mine);
+        __syncwarp();
         e0 = warps_before(mine, box, &total);
         fits = total <= kCap;
         int put = e0;
         for (int i = c0; fits && i < c1; ++i) {
-            const int n = off[i + 1] - off[i];
-            for (int b0 = 0; b0 < n; b0 += 32) {
-                const int e = b0 + lane;
-                const int2 c = e < n ? cand[(size_t)i * a.cap + e] : make_int2(0, -1);
-                const float y = __int_as_float(c.x) - m;
-                const bool take = c.y >= 0 && y > -1.f;
-                const unsigned mask = __ballot_sync(kFull, take);
-                if (take) {
-                    const int p = put + __popc(mask & ((1u << lane) - 1u));
-                    ys[p] = y;
-                    js[p] = c.y;
-                }
-                put += __popc(mask);
+            const int n = cn[i];
+            for (int e = lane; e < n; e += 32) {
+                const int2 c = cand[(size_t)i * a.cap + e];
+                ys[put + e] = __int_as_float(c.x) - m;
+                js[put + e] = c.y;
             }
+            put += n;
         }
     }
-    __syncwarp();
+    // entry i of all warps' runs in order: which of them lie where depends on the raw counts, but
+    // not the sequence of entries, so sums over i are the same from call to call
+    int ends[kSolveWarps], from[kSolveWarps];
+    auto close_up = [&](int n) {
+        __syncthreads();
+        if (lane == 0) { box[warp] = n; box2[warp] = e0; }
+        __syncthreads();
+        int sum = 0;
+#pragma unroll
+        for (int w = 0; w < kSolveWarps; ++w) {
+            from[w] = box2[w] - sum;
+            sum += box[w];
+            ends[w] = sum;
+        }
+        return sum;
+    };
+    auto where = [&](int i) {
+        int f = from[0];
+#pragma unroll
+        for (int k = 0; k + 1 < kSolveWarps; ++k)
+            if (i >= ends[k]) f = from[k + 1];
+        return f + i;
+    };
+    const int all = close_up(mine);
+    if (direct) total = all;
 
     // ---- tau - m
     const float gamma = a.gamma;
@@ -667,10 +712,10 @@ __global__ void __launch_bounds__(kSolveThreads) kv4_solve_kernel(const Kv4Args 
             F0 += t0; F1 += t1; F2 += t2;
         };
         if (fits) {
-            for (int i = lane; i < mine; i += 32) add(ys[e0 + i]);
+            for (int i = tid; i < total; i += kSolveThreads) add(ys[where(i)]);
         } else {
             for (int i = c0; i < c1; ++i) {
-                const int n = off[i + 1] - off[i];
+                const int n = cn[i];
                 for (int e = lane; e < n; e += 32) add(__int_as_float(cand[(size_t)i * a.cap + e].x) - m);
             }
         }
@@ -729,24 +774,7 @@ __global__ void __launch_bounds__(kSolveThreads) kv4_solve_kernel(const Kv4Args 
             n += __popc(mask);
             __syncwarp();
         }
-        if (lane == 0) red[0][warp] = __int_as_float(e0);
-        int sup;
-        warps_before(n, box, &sup);
-        // entry i of the support: in the run of the warp whose counts it falls into
-        int ends[kSolveWarps], from[kSolveWarps];
-#pragma unroll
-        for (int w = 0, sum = 0; w < kSolveWarps; ++w) {
-            from[w] = __float_as_int(red[0][w]) - sum;
-            sum += box[w];
-            ends[w] = sum;
-        }
-        auto where = [&](int i) {
-            int f = from[0];
-#pragma unroll
-            for (int k = 0; k + 1 < kSolveWarps; ++k)
-                if (i >= ends[k]) f = from[k + 1];
-            return f + i;
-        };
+        const int sup = close_up(n);
         constexpr int U = 8, STEP = kSolveWarps * KPW;
         for (int i0 = warp * KPW + slot; i0 < sup; i0 += U * STEP) {
             float p[U];
@@ -767,7 +795,7 @@ __global__ void __launch_bounds__(kSolveThreads) kv4_solve_kernel(const Kv4Args 
         }
     } else {
         for (int i = c0; i < c1; ++i) {
-            const int n = off[i + 1] - off[i];
+            const int n = cn[i];
             for (int e = slot; e < n; e += KPW) {
                 const int2 c = cand[(size_t)i * a.cap + e];
                 const float p = entmax_p<GM>(__int_as_float(c.x) - m - sv.tau, gamma);

@@ -49,6 +49,7 @@ COMMON = [
     (dict(page=8), capi.ENT_EINVAL),
     (dict(page=0), capi.ENT_EINVAL),
     (dict(pages=-1), capi.ENT_EINVAL),
+    (dict(pages=0), capi.ENT_EINVAL),
     (dict(max_pages=-1), capi.ENT_EINVAL),
     (dict(max_pages=1 << 27), capi.ENT_EUNSUPPORTED),
     (dict(block_table=None), capi.ENT_EINVAL),
