@@ -733,33 +733,40 @@ ent_status check_kv4(ent::Kv4Args& a, const void* kc, const void* km, const void
     return ENT_OK;
 }
 
-// Workspace of the attention: per row and run of chunks the maximum and the count, then the
-// candidates (score and key).  The rows of one key head share a scores warp, 4, 8, 16 or 32
+// Workspace of the attention: the items' run counts (an item is a block of rows of one key
+// head), per row and run its maximum, its count and its first chunk, then the candidates
+// (score and key).  The rows of one key head share a scores warp, 4, 8, 16 or 32
 // of them (the product is 8 queries wide; a warp of 4 looks its scores through with twice the
 // lanes a row; float32 rows at d = 128 take two parts each and stay at 16).
 struct Kv4Layout {
-    int block, chunk, nchunk, nsplit, cap;
-    size_t n, cand, total;
+    int block, blocks, chunk, nchunk, nslot, ctas, seqs;
+    size_t max, n, at, cand, total;
 };
 
 bool kv4_layout(const ent::Kv4Geom& g, long long rows, int group, int d, int dtype, Kv4Layout* l) {
     const long long per = (long long)g.L * group;
     l->block = per <= 4 ? 4 : per <= 8 ? 8 : per <= 16 || (dtype == ENT_F32 && d == 128) ? 16 : 32;
     if (per > 65535ll * l->block || rows > 0x7fffffffll) return false;
+    l->blocks = (int)((per + l->block - 1) / l->block);
     l->chunk = ent::kv4_chunk_keys(l->block);
     l->nchunk = ent::kv4_chunks(g, l->chunk);
-    // runs: enough warps for two rounds of 16 on each SM, no more (a longer run's later chunks
-    // are filtered by a higher maximum, and its prologue is paid once)
-    const long long blocks = (rows / (per > 0 ? per : 1)) * ((per + l->block - 1) / l->block);
-    long long want = blocks > 0 ? (2 * 16 * 148 + blocks - 1) / blocks : 1;
-    if (want > ent::kKvMaxSplit) want = ent::kKvMaxSplit;
-    if (want > l->nchunk) want = l->nchunk > 0 ? l->nchunk : 1;
-    l->nsplit = (int)want;
-    l->cap = ent::kv4_run(l->nchunk, l->nsplit) * l->chunk;
-    const size_t lists = (size_t)rows * l->nsplit;
-    l->n = round_up(lists * 4, 256);
-    l->cand = l->n + round_up(lists * 4, 256);
-    l->total = l->cand + round_up(lists * l->cap * 8, 256);
+    // one round of CTAs that stays: two on each SM, or one of the wide ones, shared out among
+    // the groups; no more than there are chunks for
+    const long long heads = per > 0 ? rows / per : 0;
+    const int groups = (g.B + ent::kKvSeqs - 1) / ent::kKvSeqs;
+    l->seqs = g.B < ent::kKvSeqs ? g.B : ent::kKvSeqs;
+    const long long chunks = groups > 0 ? heads * l->blocks * l->nchunk / groups + 1 : 1;
+    const int sms = l->block <= 8 ? 296 : 148;
+    long long want = (chunks / 2 + ent::kKvScoreWarps) / ent::kKvScoreWarps;
+    const int most = groups > 0 ? (sms + groups - 1) / groups : 1;
+    l->ctas = (int)(want < most ? want : most);
+    l->nslot = l->ctas * ent::kKvScoreWarps < l->nchunk ? l->ctas * ent::kKvScoreWarps : l->nchunk;
+    const size_t runs = (size_t)rows * l->nslot * 4;
+    l->max = round_up((size_t)heads * l->blocks * 4, 256);
+    l->n = l->max + round_up(runs, 256);
+    l->at = l->n + round_up(runs, 256);
+    l->cand = l->at + round_up(runs, 256);
+    l->total = l->cand + round_up((size_t)rows * l->nchunk * l->chunk * 8, 256);
     return true;
 }
 
@@ -853,11 +860,13 @@ ent_status ent_attn_kv4_fwd(const void* q, int B, int Hq, int Hkv, int L, int d,
     a.alpha = alpha;
     const int gm = gamma_mode(alpha, &a.gamma);
     a.cx = (alpha - 1.f) / sqrtf((float)d);
-    a.block = l.block; a.chunk = l.chunk; a.nchunk = l.nchunk;
-    a.nsplit = l.nsplit; a.cap = l.cap;
+    a.block = l.block; a.blocks = l.blocks; a.chunk = l.chunk; a.nchunk = l.nchunk;
+    a.nslot = l.nslot; a.ctas = l.ctas; a.seqs = l.seqs;
     char* base = static_cast<char*>(ws);
-    a.split_max = reinterpret_cast<float*>(base);
-    a.split_n = reinterpret_cast<int*>(base + l.n);
+    a.item_n = reinterpret_cast<int*>(base);
+    a.run_max = reinterpret_cast<float*>(base + l.max);
+    a.run_n = reinterpret_cast<int*>(base + l.n);
+    a.run_at = reinterpret_cast<int*>(base + l.at);
     a.cand = reinterpret_cast<int2*>(base + l.cand);
     cudaError_t e = ent::kv4_attn(a, d, dtype == ENT_BF16, gm, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? ENT_OK : cuda_fail(e, "cache attention launch");

@@ -139,15 +139,20 @@ struct Kv4Args {
     void* o;
     float* tau;                 // nullable [B][Hkv * group][L], x units
     float alpha, gamma, cx;     // as in FwdArgs
-    int block;                  // query rows of a scores warp (4, 8, 16 or 32)
-    int chunk, nchunk;          // keys of a chunk, chunks of a call
-    int nsplit, cap;            // runs of chunks, one scores warp each; keys of the longest run
-    float* split_max;           // workspace: [rows][nsplit], rows = B Hkv L group
-    int* split_n;               //            [rows][nsplit]
-    int2* cand;                 //            [rows][nsplit][cap]: score bits, key
+    int block, blocks;          // query rows of a scores warp (4, 8, 16 or 32), such blocks of a key head
+    int chunk, nchunk;          // keys of a chunk, most chunks of a sequence
+    int nslot;                  // most runs (a worker's share of an item) of an item
+    int ctas, seqs;             // scores CTAs a group of sequences, sequences a group
+    int* item_n;                // workspace: [B Hkv][blocks] runs of the item
+    float* run_max;             //            [rows][nslot], rows = B Hkv L group
+    int* run_n;                 //            [rows][nslot]
+    int* run_at;                //            [rows][nslot] first chunk
+    int2* cand;                 //            [rows][nchunk * chunk]: score bits, key; a run's from run_at on
 };
 __host__ __device__ constexpr int kv4_chunk_keys(int block) { return block == 32 ? 32 : 64; }
-constexpr int kKvMaxSplit = 1024;
+constexpr int kKvSeqs = 256;          // sequences of a group (one thread each)
+constexpr int kKvScoreWarps = 8;      // warps of a scores CTA
+constexpr int kKvMaxRuns = 296 * kKvScoreWarps;
 cudaError_t kv4_write(const Kv4Args& a, int d, bool bf16, cudaStream_t s);
 cudaError_t kv4_read(const Kv4Args& a, int d, bool bf16, cudaStream_t s);
 cudaError_t kv4_attn(const Kv4Args& a, int d, bool bf16, int gm, cudaStream_t s);

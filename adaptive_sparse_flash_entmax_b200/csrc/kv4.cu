@@ -242,8 +242,9 @@ __device__ __forceinline__ void load_words(const uint32_t* p, uint32_t (&w)[G]) 
     }
 }
 
-constexpr int kScoreThreads = 256;
-constexpr int kScoreWarps = kScoreThreads / 32;
+constexpr int kScoreWarps = kKvScoreWarps;
+constexpr int kScoreThreads = kScoreWarps * 32;
+static_assert(kScoreThreads == kKvSeqs, "a thread per sequence of the group");
 
 // R: rows of a block (4, 8, 16 or 32), in NT products of 8 columns.
 template <typename T, int D, int R>
@@ -253,108 +254,76 @@ __global__ void __launch_bounds__(kScoreThreads, R <= 8 ? 2 : 1) kv4_scores_kern
     constexpr int kStride = C + 4;   // spreads a product's 8 keys x 4 row pairs over the banks
     constexpr bool F32 = sizeof(T) == 4;
     __shared__ __align__(16) float xs_all[kScoreWarps][8 * NT * kStride];
-    __shared__ float row_max[R];
+    __shared__ unsigned long long pub[kScoreWarps][R];   // item << 32 | the row's maximum so far
+    __shared__ long long pre[kKvSeqs + 1];               // chunks of the group before each sequence
+    __shared__ long long warp_sum[kScoreWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     float* xs = xs_all[warp];
-    const int bk = blockIdx.z, b = bk / a.Hkv, hk = bk - b * a.Hkv;
-    const Kv4Seq s = seq_of(a, b);
-    if (s.bad && a.bad && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(a.bad, s.bad);
-    const int row0 = blockIdx.y * R, nrows = s.rows * a.group;   // real rows of this key head
-    const int nch = kv4_seq_chunks(a.g, s, C), run = kv4_run(nch, a.nsplit);
-    const int split = blockIdx.x * kScoreWarps + warp;
-    const int ch0 = split * run, ch1 = kv4_min(ch0 + run, nch);
-    if (threadIdx.x < R) row_max[threadIdx.x] = -INFINITY;
-    __syncthreads();
-    if (row0 >= nrows || ch0 >= ch1) return;   // (the solver takes no more runs than hold a chunk)
 
-    // ---- queries: lane (n = lane / 4, c = lane % 4) holds dimensions 32 w + 8 c + i of row n
-    const int c = lane & 3;
-    uint32_t qf[NT][G][4], ql[F32 ? NT : 1][G][4];   // B operands; float32 rows: high and low parts
-    uint32_t qz[NT][3];                              // sum q of group c in three parts
-    // the row that this lane looks through, in its lanes' part `sub`, and its factors
-    const int lrow = lane / LPR, sub = lane % LPR;
-    float mul = 0.f, mul2 = 0.f;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        const int r = row0 + nt * 8 + (lane >> 2);
-        const bool real = r < nrows && nt * 8 + (lane >> 2) < R;
-        const int l = real ? r / a.group : 0, gi = real ? r - l * a.group : 0;
-        const T* q = static_cast<const T*>(a.q) + (((size_t)b * a.Hkv * a.group + hk * a.group + gi) * a.g.L + l) * D;
-        float x[G][8];
-        float top = 0.f;
-        bool fine = true;
-#pragma unroll
-        for (int w = 0; w < G; ++w) {
-            if (real) load8(q + 32 * w + 8 * c, x[w]);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if (!real) x[w][i] = 0.f;
-                fine &= isfinite(x[w][i]);
-                top = fmaxf(top, fabsf(x[w][i]));
-            }
+    // ---- the group's work, and this warp's share of it
+    const int b0 = blockIdx.y * a.seqs, nseq = kv4_min(a.seqs, a.g.B - b0);
+    {
+        const int i = threadIdx.x;
+        long long n = 0;
+        if (i < nseq) {
+            const Kv4Seq s = seq_of(a, b0 + i);
+            if (s.bad && a.bad && blockIdx.x == 0) atomicOr(a.bad, s.bad);
+            if (s.rows > 0)
+                n = (long long)kv4_seq_chunks(a.g, s, C) * a.Hkv * ((s.rows * a.group + R - 1) / R);
         }
+        long long incl = n;
 #pragma unroll
-        for (int o = 1; o < 4; o <<= 1) {
-            top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-            fine &= __shfl_xor_sync(kFull, (int)fine, o) != 0;
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(kFull, incl, o);
+            if (lane >= o) incl += y;
         }
-        int e = 0;
-        if (top > 0.f && fine) { frexpf(top, &e); e = 15 - e; }
-        const float fe1 = ldexpf(1.f, e / 2), fe2 = ldexpf(1.f, e - e / 2);
-        float zsum = 0.f;
-#pragma unroll
-        for (int w = 0; w < G; ++w) {
-            float sum = 0.f, hi[8], lo[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float y = x[w][i] * fe1 * fe2;   // 2^e in two exact steps
-                hi[i] = __half2float(__float2half_rn(y));
-                lo[i] = y - hi[i];
-                sum += y;
-            }
-            const float f = 0.0625f;
-            qf[nt][w][0] = pack_half(hi[0], hi[4]);
-            qf[nt][w][1] = pack_half(hi[1] * f, hi[5] * f);
-            qf[nt][w][2] = pack_half(hi[2], hi[6]);
-            qf[nt][w][3] = pack_half(hi[3] * f, hi[7] * f);
-            if constexpr (F32) {
-                ql[nt][w][0] = pack_half(lo[0], lo[4]);
-                ql[nt][w][1] = pack_half(lo[1] * f, lo[5] * f);
-                ql[nt][w][2] = pack_half(lo[2], lo[6]);
-                ql[nt][w][3] = pack_half(lo[3] * f, lo[7] * f);
-            }
-            sum += __shfl_xor_sync(kFull, sum, 1);
-            sum += __shfl_xor_sync(kFull, sum, 2);
-            if (w == c) zsum = sum * 5.9604644775390625e-08f;   // 2^-24, the codes' unit
-        }
-        qz[nt][0] = bf16_part(zsum);
-        qz[nt][1] = bf16_part(zsum);
-        qz[nt][2] = bf16_part(zsum);
-        // x = cx 2^(24 - e) s: in two factors, either of which is in range
-        const int e1 = (24 - e) / 2;
-        // a row with a NaN or an infinity has NaN scores
-        const float f1 = fine ? a.cx * ldexpf(1.f, e1) : nanf(""), f2 = ldexpf(1.f, 24 - e - e1);
-        const float g1 = __shfl_sync(kFull, f1, 4 * (lrow & 7)), g2 = __shfl_sync(kFull, f2, 4 * (lrow & 7));
-        if (lrow >> 3 == nt) { mul = g1; mul2 = g2; }
+        if (lane == 31) warp_sum[warp] = incl;
+        if (lane < R) pub[warp][lane] = ~0ull;
+        __syncthreads();
+        for (int w = 0; w < warp; ++w) incl += warp_sum[w];
+        pre[i + 1] = incl;
+        if (i == 0) pre[0] = 0;
+        __syncthreads();
     }
+    const long long T_all = pre[nseq];
+    const int W = kv4_workers(T_all, gridDim.x * kScoreWarps), worker = blockIdx.x * kScoreWarps + warp;
+    if (worker >= W) return;
+    long long x0 = kv4_share(T_all, W, worker);
+    const long long x1 = kv4_share(T_all, W, worker + 1);
 
-    // ---- keys, a chunk of U tiles at a time
-    const int* table = a.table + (size_t)b * a.g.max_pages;
-    const int key = lane >> 2;   // the lane's keys of a tile: key and key + 8
-    const bool lreal = row0 + lrow < nrows;
-    const int lpos = lreal ? s.start + (row0 + lrow) / a.group : -1;
-    const size_t list = ((size_t)bk * a.g.L * a.group + row0 + lrow) * a.nsplit + split;
-    int2* out = a.cand + list * a.cap;
-    const int pos_first = s.start + row0 / a.group;
-    const int pos_last = s.start + (kv4_min(row0 + R, nrows) - 1) / a.group;
-    float m = -INFINITY;    // of the row, over the run so far
-    int n = 0;              // candidates of the row so far
+    const int c = lane & 3, key = lane >> 2;   // the lane's keys of a tile: key and key + 8
+    const int lrow = lane / LPR, sub = lane % LPR;   // the row that it looks through, and its part of it
+    constexpr int kTokenB = D / 2, kMetaB = 4 * G;   // bytes of a token
+    const size_t page_rows = (size_t)a.Hkv << a.g.page_shift;
+    const int mask = (1 << a.g.page_shift) - 1;
+
+#pragma unroll 1
+    while (x0 < x1) {
+    // ---- the item that chunk x0 belongs to, and the run of it that is this warp's
+    int i = 0;
+#pragma unroll
+    for (int step = kKvSeqs / 2; step > 0; step >>= 1)
+        if (i + step < nseq && pre[i + step] <= x0) i += step;
+    const int b = b0 + i;
+    const Kv4Seq s = seq_of(a, b);
+    const int nrows = s.rows * a.group, nch = kv4_seq_chunks(a.g, s, C), nblk = (nrows + R - 1) / R;
+    const long long rem = x0 - pre[i];
+    const int it = (int)(rem / nch), ch0 = (int)(rem - (long long)it * nch);
+    const int hk = it / nblk, blk = it - hk * nblk, row0 = blk * R;
+    const int ch1 = (int)(x1 - x0 < nch - ch0 ? ch0 + (x1 - x0) : nch);
+    const long long item0 = x0 - ch0;
+    const int first_worker = kv4_worker(T_all, W, item0), slot = worker - first_worker;
+    const unsigned item = (unsigned)(b * a.Hkv + hk) * (unsigned)a.blocks + (unsigned)blk;
+    if (ch0 == 0 && lane == 0) a.item_n[item] = kv4_worker(T_all, W, item0 + nch - 1) - first_worker + 1;
+    x0 += ch1 - ch0;
+
     // chunk ch holds keys k0 .. k1-1 (kv4_chunk, with what does not change taken out)
+    const int* table = a.table + (size_t)b * a.g.max_pages;
     const int ns = kv4_sink_chunks(a.g, C), sink_end = kv4_min(kv4_sink_end(a.g), s.end);
     const int base = kv4_base(a.g, s.start) - ns * C;
     auto first_key = [&](int ch) { return ch * C + (ch < ns ? 0 : base); };
     auto end_key = [&](int ch, int k0) { return kv4_min(k0 + C, ch < ns ? sink_end : s.end); };
-    // page of tile `lane` of a chunk (lanes below U), one chunk ahead of its loads
+    // page of tile `lane` of a chunk (lanes below U)
     auto page_of = [&](int ch) {
         int p = -1;
         if (ch < ch1 && lane < U) {
@@ -366,25 +335,18 @@ __global__ void __launch_bounds__(kScoreThreads, R <= 8 ? 2 : 1) kv4_scores_kern
         }
         return p;
     };
-    // bytes: of a token, of a page of all heads, and the lane's place in this head's page
-    constexpr int kTokenB = D / 2, kMetaB = 4 * G;
-    const size_t page_b = (size_t)a.Hkv << a.g.page_shift;
-    const int mask = (1 << a.g.page_shift) - 1;
     const char* lane_codes = reinterpret_cast<const char*>(a.k_codes) +
                              (((size_t)hk << a.g.page_shift) + key) * kTokenB + c * 4 * G;
-    const char* lane_meta = reinterpret_cast<const char*>(a.k_meta) +
-                            (((size_t)hk << a.g.page_shift) + key) * kMetaB;
-    int pages = page_of(ch0);
-#pragma unroll 1
-    for (int ch = ch0; ch < ch1; ++ch) {
-        const int k0 = first_key(ch), k1 = end_key(ch, k0);
-        uint32_t w[U][2][G], mt[U][2][G];
-        const unsigned has = __ballot_sync(kFull, pages >= 0);
+    const char* lane_meta = reinterpret_cast<const char*>(a.k_meta) + (((size_t)hk << a.g.page_shift) + key) * kMetaB;
+    uint32_t w[U][2][G], mt[U][2][G];
+    // a chunk's tiles into w and mt; a tile that is not there reads the pool's first page
+    // instead, and no row sees it.  Returns which tiles are there.
+    auto load_chunk = [&](int ch, int pages) {
+        const int k0 = first_key(ch);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            // a tile that is not there reads the pool's first page instead, and no row sees it
             const int page = max(__shfl_sync(kFull, pages, u), 0);
-            const size_t row = page * page_b + ((k0 + u * kKvTile) & mask);
+            const size_t row = page * page_rows + ((k0 + u * kKvTile) & mask);
             const char* pc = lane_codes + row * kTokenB;
             const char* pm = lane_meta + row * kMetaB;
 #pragma unroll
@@ -393,7 +355,98 @@ __global__ void __launch_bounds__(kScoreThreads, R <= 8 ? 2 : 1) kv4_scores_kern
                 load_words<G>(reinterpret_cast<const uint32_t*>(pm + 8 * h * kMetaB), mt[u][h]);
             }
         }
-        pages = page_of(ch + 1);
+        return __ballot_sync(kFull, pages >= 0);
+    };
+    unsigned has = load_chunk(ch0, page_of(ch0));
+    int pages = page_of(ch0 + 1);
+
+    // ---- queries: lane (n = lane / 4, c = lane % 4) holds dimensions 32 w + 8 c + i of row n
+    uint32_t qf[NT][G][4], ql[F32 ? NT : 1][G][4];   // B operands; float32 rows: high and low parts
+    uint32_t qz[NT][3];                              // sum q of group c in three parts
+    float mul = 0.f, mul2 = 1.f;                     // of row lrow: x = mul mul2 acc
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const int r = row0 + nt * 8 + key;
+        const bool real = r < nrows && nt * 8 + key < R;
+        const int l = real ? r / a.group : 0, gi = real ? r - l * a.group : 0;
+        const T* q = static_cast<const T*>(a.q) + (((size_t)b * a.Hkv * a.group + hk * a.group + gi) * a.g.L + l) * D;
+        float x[G][8];
+        float top = 0.f;
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            if (real) load8(q + 32 * g + 8 * c, x[g]);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                if (!real) x[g][k] = 0.f;
+                top = max_nan(top, fabsf(x[g][k]));
+            }
+        }
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) top = max_nan(top, __shfl_xor_sync(kFull, top, o));
+        const bool fine = top < INFINITY;
+        int e = 0;
+        // (2^126 at most: a row below 2^-111 is held to 2^-150)
+        if (top > 0.f && fine) { frexpf(top, &e); e = min(15 - e, 126); }
+        const float fe = __int_as_float((e + 127) << 23);
+        float zsum = 0.f;
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            float sum = 0.f, y[8], lo[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                y[k] = x[g][k] * fe;
+                sum += y[k];
+            }
+            if constexpr (F32) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const float hi = __half2float(__float2half_rn(y[k]));
+                    lo[k] = y[k] - hi;
+                    y[k] = hi;
+                }
+            }
+            const float f = 0.0625f;
+            qf[nt][g][0] = pack_half(y[0], y[4]);
+            qf[nt][g][1] = pack_half(y[1] * f, y[5] * f);
+            qf[nt][g][2] = pack_half(y[2], y[6]);
+            qf[nt][g][3] = pack_half(y[3] * f, y[7] * f);
+            if constexpr (F32) {
+                ql[nt][g][0] = pack_half(lo[0], lo[4]);
+                ql[nt][g][1] = pack_half(lo[1] * f, lo[5] * f);
+                ql[nt][g][2] = pack_half(lo[2], lo[6]);
+                ql[nt][g][3] = pack_half(lo[3] * f, lo[7] * f);
+            }
+            sum += __shfl_xor_sync(kFull, sum, 1);
+            sum += __shfl_xor_sync(kFull, sum, 2);
+            if (g == c) zsum = sum * 5.9604644775390625e-08f;   // 2^-24, the codes' unit
+        }
+        qz[nt][0] = bf16_part(zsum);
+        qz[nt][1] = bf16_part(zsum);
+        qz[nt][2] = bf16_part(zsum);
+        // x = cx 2^(24 - e) s, in two factors where one would overflow (24 - e <= 137);
+        // a row with a NaN or an infinity has NaN scores
+        const int e1 = min(24 - e, 100);
+        const float f1 = fine ? a.cx * __int_as_float((e1 + 127) << 23) : nanf("");
+        const float f2 = __int_as_float((24 - e - e1 + 127) << 23);
+        const float g1 = __shfl_sync(kFull, f1, 4 * (lrow & 7)), g2 = __shfl_sync(kFull, f2, 4 * (lrow & 7));
+        if (lrow >> 3 == nt) { mul = g1; mul2 = g2; }
+    }
+
+    const bool lreal = row0 + lrow < nrows;
+    const int lpos = lreal ? s.start + (row0 + lrow) / a.group : -1;
+    const size_t grow = ((size_t)b * a.Hkv + hk) * a.g.L * a.group + row0 + lrow;   // the lane's row
+    int2* out = a.cand + (grow * a.nchunk + ch0) * C;
+    const int pos_first = s.start + row0 / a.group;
+    const int pos_last = s.start + (kv4_min(row0 + R, nrows) - 1) / a.group;
+    float m = -INFINITY;    // of the row, over the run so far (and what other warps told)
+    int n = 0;              // candidates of the row so far
+    volatile unsigned long long* mine = &pub[warp][lrow];
+    if (sub == 0) *mine = (unsigned long long)item << 32 | 0xff800000u;
+
+    // ---- keys, a chunk of U tiles at a time
+#pragma unroll 1
+    for (int ch = ch0; ch < ch1; ++ch) {
+        const int k0 = first_key(ch), k1 = end_key(ch, k0);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             float acc[NT][4];
@@ -402,7 +455,7 @@ __global__ void __launch_bounds__(kScoreThreads, R <= 8 ? 2 : 1) kv4_scores_kern
             for (int h = 0; h < 2; ++h) {
                 mz[h] = c == 0 ? mt[u][h][0] : 0u;
 #pragma unroll
-                for (int i = 1; i < G; ++i) mz[h] = c == i ? mt[u][h][i] : mz[h];
+                for (int g = 1; g < G; ++g) mz[h] = c == g ? mt[u][h][g] : mz[h];
             }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
@@ -410,23 +463,23 @@ __global__ void __launch_bounds__(kScoreThreads, R <= 8 ? 2 : 1) kv4_scores_kern
                 mma_1688_bf(acc[nt], mz[0], mz[1], qz[nt][2]);
             }
 #pragma unroll
-            for (int i = 0; i < G; ++i) {
-                uint32_t w0 = w[u][0][i], w1 = w[u][1][i];
+            for (int g = 0; g < G; ++g) {
+                uint32_t w0 = w[u][0][g], w1 = w[u][1][g];
                 uint32_t av[8];
                 av[0] = w0 & 0x000f000fu; av[1] = w1 & 0x000f000fu;
                 av[2] = w0 & 0x00f000f0u; av[3] = w1 & 0x00f000f0u;
                 w0 >>= 8; w1 >>= 8;
                 av[4] = w0 & 0x000f000fu; av[5] = w1 & 0x000f000fu;
                 av[6] = w0 & 0x00f000f0u; av[7] = w1 & 0x00f000f0u;
-                const float s0 = bf16_lo(mt[u][0][i]), s1 = bf16_lo(mt[u][1][i]);
+                const float s0 = bf16_lo(mt[u][0][g]), s1 = bf16_lo(mt[u][1][g]);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     float d[4];
-                    mma_16816_0(d, av[0], av[1], av[2], av[3], qf[nt][i][0], qf[nt][i][1]);
-                    mma_16816(d, av[4], av[5], av[6], av[7], qf[nt][i][2], qf[nt][i][3]);
+                    mma_16816_0(d, av[0], av[1], av[2], av[3], qf[nt][g][0], qf[nt][g][1]);
+                    mma_16816(d, av[4], av[5], av[6], av[7], qf[nt][g][2], qf[nt][g][3]);
                     if constexpr (F32) {
-                        mma_16816(d, av[0], av[1], av[2], av[3], ql[nt][i][0], ql[nt][i][1]);
-                        mma_16816(d, av[4], av[5], av[6], av[7], ql[nt][i][2], ql[nt][i][3]);
+                        mma_16816(d, av[0], av[1], av[2], av[3], ql[nt][g][0], ql[nt][g][1]);
+                        mma_16816(d, av[4], av[5], av[6], av[7], ql[nt][g][2], ql[nt][g][3]);
                     }
                     acc[nt][0] = fmaf(s0, d[0], acc[nt][0]);
                     acc[nt][1] = fmaf(s0, d[1], acc[nt][1]);
@@ -443,41 +496,51 @@ __global__ void __launch_bounds__(kScoreThreads, R <= 8 ? 2 : 1) kv4_scores_kern
                         xs[(nt * 8 + 2 * c + k) * kStride + u * kKvTile + key + 8 * h] = acc[nt][2 * h + k];
         }
         __syncwarp();
+        // not every row sees every key of the chunk: those it does not see leave as -inf
+        const unsigned there = has;
+        const bool whole = there == (1u << U) - 1u && k1 - k0 == C && k1 - 1 <= pos_first &&
+                           (!a.g.window || k1 <= a.g.sinks || k0 > pos_last - a.g.window);
+        // the next chunk's loads are on their way while the rows are looked through
+        if (ch + 1 < ch1) {
+            has = load_chunk(ch + 1, pages);
+            pages = page_of(ch + 2);
+        }
         // ---- the row's part of the chunk: keys (i * LPR + sub) * 4 + e
         float v[KPL];
 #pragma unroll
-        for (int i = 0; i < KPL / 4; ++i) {
-            const float4 f = *reinterpret_cast<const float4*>(xs + lrow * kStride + (i * LPR + sub) * 4);
-            v[4 * i] = f.x * mul * mul2; v[4 * i + 1] = f.y * mul * mul2;
-            v[4 * i + 2] = f.z * mul * mul2; v[4 * i + 3] = f.w * mul * mul2;
+        for (int k = 0; k < KPL / 4; ++k) {
+            const float4 f = *reinterpret_cast<const float4*>(xs + lrow * kStride + (k * LPR + sub) * 4);
+            v[4 * k] = f.x * mul; v[4 * k + 1] = f.y * mul; v[4 * k + 2] = f.z * mul; v[4 * k + 3] = f.w * mul;
         }
-        __syncwarp();
-        // not every row sees every key of the chunk: those it does not see leave as -inf
-        const bool whole = has == (1u << U) - 1u && k1 - k0 == C && k1 - 1 <= pos_first &&
-                           (!a.g.window || k1 <= a.g.sinks || k0 > pos_last - a.g.window);
+        if (mul2 != 1.f) {
+#pragma unroll
+            for (int k = 0; k < KPL; ++k) v[k] *= mul2;
+        }
         if (!whole) {
 #pragma unroll
-            for (int i = 0; i < KPL; ++i) {
-                const int kk = ((i >> 2) * LPR + sub) * 4 + (i & 3);
-                const bool see = k0 + kk < k1 && (has >> (kk / kKvTile) & 1u) && kv4_sees(a.g, lpos, k0 + kk);
-                v[i] = see ? v[i] : -INFINITY;
+            for (int k = 0; k < KPL; ++k) {
+                const int kk = ((k >> 2) * LPR + sub) * 4 + (k & 3);
+                const bool see = k0 + kk < k1 && (there >> (kk / kKvTile) & 1u) && kv4_sees(a.g, lpos, k0 + kk);
+                v[k] = see ? v[k] : -INFINITY;
             }
         }
-        // a NaN passes through every maximum; +inf is caught at the end.  (A store that loses to
-        // another warp's costs a weaker filter, no more.)
-        m = max_nan(m, *const_cast<volatile float*>(&row_max[lrow]));
+        // a NaN passes through every maximum; +inf is caught at the end
+        for (int o = sub; o < kScoreWarps; o += LPR) {
+            const unsigned long long p = *const_cast<volatile unsigned long long*>(&pub[o][lrow]);
+            if ((unsigned)(p >> 32) == item) m = max_nan(m, __uint_as_float((unsigned)p));
+        }
 #pragma unroll
-        for (int i = 0; i < KPL; ++i) m = max_nan(m, v[i]);
+        for (int k = 0; k < KPL; ++k) m = max_nan(m, v[k]);
 #pragma unroll
         for (int o = 1; o < LPR; o <<= 1) m = max_nan(m, __shfl_xor_sync(kFull, m, o));
-        if (sub == 0) *const_cast<volatile float*>(&row_max[lrow]) = m;
+        if (sub == 0) *mine = (unsigned long long)item << 32 | __float_as_uint(m);
         // above m - 1, and the maximum itself: where |m| >= 2^24 makes them equal, the limit is
         // the next float below m (m = -inf or NaN: it is NaN, and nothing is above)
         float lim = m - 1.f;
         if (!(lim < m)) lim = __int_as_float(__float_as_int(m) + (m > 0.f ? -1 : 1));
         unsigned take = 0;
 #pragma unroll
-        for (int i = 0; i < KPL; ++i) take |= (v[i] > lim ? 1u : 0u) << i;
+        for (int k = 0; k < KPL; ++k) take |= (v[k] > lim ? 1u : 0u) << k;
         if (!lreal) take = 0;
         const int cnt = __popc(take);
         int incl = cnt;
@@ -488,16 +551,24 @@ __global__ void __launch_bounds__(kScoreThreads, R <= 8 ? 2 : 1) kv4_scores_kern
         }
         int put = n + incl - cnt;
         n += __shfl_sync(kFull, incl, LPR - 1, LPR);
-#pragma unroll
-        for (int i = 0; i < KPL; ++i)
-            if (take >> i & 1u)
-                out[put++] = make_int2(__float_as_int(v[i]), k0 + ((i >> 2) * LPR + sub) * 4 + (i & 3));
+        // (few lanes have more than one or two: read again what is taken, rather than hold every
+        // value against its bit)
+        while (take) {
+            const int k = __ffs(take) - 1;
+            take &= take - 1u;
+            const int kk = ((k >> 2) * LPR + sub) * 4 + (k & 3);
+            out[put++] = make_int2(__float_as_int(xs[lrow * kStride + kk] * mul * mul2), k0 + kk);
+        }
+        __syncwarp();
     }
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (lreal && sub == 0) {
-        a.split_max[list] = m < INFINITY ? m : nanf("");
-        a.split_n[list] = n;
+        a.run_max[grow * a.nslot + slot] = m < INFINITY ? m : nanf("");
+        a.run_n[grow * a.nslot + slot] = n;
+        a.run_at[grow * a.nslot + slot] = ch0;
     }
+    __syncwarp();
+    }   // items of this warp's share
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // ------------------------------------------------------------------ solve and P.V
@@ -508,7 +579,7 @@ __global__ void __launch_bounds__(kScoreThreads, R <= 8 ? 2 : 1) kv4_scores_kern
 // relative to m, so tau keeps its precision for scores of any size.  Every sum has a fixed
 // order: the result does not change from run to run.  A row with more than kCap candidates
 // even above m - 1 goes over the runs' lists again in every pass.
-constexpr int kSolveThreads = 128;
+constexpr int kSolveThreads = 256;
 constexpr int kSolveWarps = kSolveThreads / 32;
 constexpr int kCap = 4096;
 constexpr float kKvFtol = 2e-7f, kKvStol = 6e-8f;   // to the rounding of the sums
@@ -538,9 +609,11 @@ __device__ __forceinline__ int warps_before(int n, int* box, int* all) {
 template <typename T, int D, int GM>
 __global__ void __launch_bounds__(kSolveThreads) kv4_solve_kernel(const Kv4Args a) {
     constexpr int G = D / kKvGroup, LPK = D / 8, KPW = 32 / LPK;
-    __shared__ float ys[kCap];          // x - m of the candidates, then their weights
-    __shared__ int js[kCap];            // their keys
-    __shared__ int off[kKvMaxSplit + 1];   // the runs' candidates before each run
+    extern __shared__ int solve_smem[];
+    float* ys = reinterpret_cast<float*>(solve_smem);   // [kCap] x - m of the candidates, then their weights
+    int* js = solve_smem + kCap;                        // [kCap] their keys
+    int* lst = js + kCap;               // [nslot] where the runs' lists begin in the row's part of the workspace
+    int* off = lst + a.nslot;           // [nslot + 1] the runs' candidates before each run
     __shared__ float red[3][kSolveWarps];
     __shared__ int box[kSolveWarps], box2[kSolveWarps];
     __shared__ float bc[2];
@@ -553,16 +626,15 @@ __global__ void __launch_bounds__(kSolveThreads) kv4_solve_kernel(const Kv4Args 
     const Kv4Seq s = seq_of(a, b);
     const size_t orow = ((size_t)b * a.Hkv * a.group + hk * a.group + gi) * a.g.L + l;
     T* o = static_cast<T*>(a.o) + orow * D;
-    int nrun = 0;
-    if (l < s.rows) {
-        const int nch = kv4_seq_chunks(a.g, s, a.chunk), run = kv4_run(nch, a.nsplit);
-        nrun = run > 0 ? (nch + run - 1) / run : 0;
-    }
-    const size_t at = ((size_t)bk * per + r) * a.nsplit;
-    const float* cm = a.split_max + at;
-    const int* cn = a.split_n + at;
-    const int2* cand = a.cand + at * a.cap;
+    const size_t at = ((size_t)bk * per + r) * a.nslot;
+    const float* cm = a.run_max + at;
+    int* cn = a.run_n + at;
+    const int* cat = a.run_at + at;
+    int2* cand = a.cand + ((size_t)bk * per + r) * a.nchunk * a.chunk;
+    auto list_of = [&](int i) { return cand + lst[i]; };
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    const bool seen = l < s.rows && kv4_seq_chunks(a.g, s, a.chunk) > 0;
+    const int nrun = seen ? a.item_n[(size_t)bk * a.blocks + r / a.block] : 0;
 
     // ---- row maximum (every warp for itself), then the runs' offsets, a quarter each warp
     float m = -INFINITY;
@@ -593,7 +665,10 @@ __global__ void __launch_bounds__(kSolveThreads) kv4_solve_kernel(const Kv4Args 
             const int y = __shfl_up_sync(kFull, incl, d);
             if (lane >= d) incl += y;
         }
-        if (i < c1) off[i] = sum + incl - n;
+        if (i < c1) {
+            off[i] = sum + incl - n;
+            lst[i] = cat[i] * a.chunk;   // (a row's part holds at most 2^30 entries)
+        }
         sum += __shfl_sync(kFull, incl, 31);
     }
     int raw;
@@ -602,46 +677,60 @@ __global__ void __launch_bounds__(kSolveThreads) kv4_solve_kernel(const Kv4Args 
     if (tid == 0) off[nrun] = raw;
     __syncthreads();
 
-    // ---- candidates: each warp holds a run [e0, e0 + mine) of the arrays
+    // ---- candidates above m - 1, in order, into shared memory: each warp takes its part of all
+    // runs' entries as one sequence.  Where the sequence fits, the kept ones stay within the
+    // warp's part of the arrays; else they are counted first and then placed.
     const bool direct = raw <= kCap;
-    bool fits = true;
-    int e0, mine = 0, total;
-    if (direct) {
-        e0 = (int)((long long)raw * warp / kSolveWarps);
-        const int e1 = (int)((long long)raw * (warp + 1) / kSolveWarps);
-        int i = 0;   // the run that holds entry e0 (by halving), then forward
-        for (int step = kKvMaxSplit; step > 0; step >>= 1)
-            if (i + step < nrun && off[i + step] <= e0) i += step;
+    const int part0 = (int)((long long)raw * warp / kSolveWarps), part1 = (int)((long long)raw * (warp + 1) / kSolveWarps);
+    // calls f(y, key, lanes that keep theirs) for 32 entries of the part at a time
+    auto each = [&](auto f) {
+        int i = 0;   // the run that holds entry part0 (by halving), then forward
+#pragma unroll 1
+        for (int step = 2048; step > 0; step >>= 1)
+            if (i + step < nrun && off[i + step] <= part0) i += step;
         constexpr int U = 4;
-        for (int base = e0; base < e1; base += 32 * U) {
+#pragma unroll 1
+        for (int base = part0; base < part1; base += 32 * U) {
             int2 c[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int e = base + u * 32 + lane;
                 c[u] = make_int2(0, -1);
-                if (e < e1) {
+                if (e < part1) {
                     while (off[i + 1] <= e) ++i;
-                    c[u] = cand[(size_t)i * a.cap + (e - off[i])];
+                    c[u] = list_of(i)[e - off[i]];
                 }
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const float y = __int_as_float(c[u].x) - m;
                 const bool take = c[u].y >= 0 && y > -1.f;
-                const unsigned mask = __ballot_sync(kFull, take);
-                if (take) {
-                    const int p = e0 + mine + __popc(mask & ((1u << lane) - 1u));
-                    ys[p] = y;
-                    js[p] = c[u].y;
-                }
-                mine += __popc(mask);
+                f(y, c[u].y, take, __ballot_sync(kFull, take));
             }
         }
-    } else {
+    };
+    int e0 = part0, mine = 0, total = 0;
+    bool fits = true;
+    if (!direct) {
+        each([&](float, int, bool, unsigned mask) { mine += __popc(mask); });
+        e0 = warps_before(mine, box, &total);
+        fits = total <= kCap;
+        mine = 0;
+    }
+    if (fits)
+        each([&](float y, int j, bool take, unsigned mask) {
+            if (take) {
+                const int p = e0 + mine + __popc(mask & ((1u << lane) - 1u));
+                ys[p] = y;
+                js[p] = j;
+            }
+            mine += __popc(mask);
+        });
+    else
         // each warp closes up its own lists in the workspace, so that what follows does not
-        // depend on what the scores kernel left in them
+        // depend on what else the scores kernel left in them
         for (int i = c0; i < c1; ++i) {
-            int2* list = a.cand + (at + i) * a.cap;
+            int2* list = list_of(i);
             const int n = off[i + 1] - off[i];
             int kept = 0;
             for (int b0 = 0; b0 < n; b0 += 32) {
@@ -653,23 +742,10 @@ __global__ void __launch_bounds__(kSolveThreads) kv4_solve_kernel(const Kv4Args 
                 kept += __popc(mask);
                 __syncwarp();
             }
-            if (lane == 0) a.split_n[at + i] = kept;
-            mine += kept;
+            __syncwarp();
+            if (lane == 0) cn[i] = kept;
+            __syncwarp();
         }
-        __syncwarp();
-        e0 = warps_before(mine, box, &total);
-        fits = total <= kCap;
-        int put = e0;
-        for (int i = c0; fits && i < c1; ++i) {
-            const int n = cn[i];
-            for (int e = lane; e < n; e += 32) {
-                const int2 c = cand[(size_t)i * a.cap + e];
-                ys[put + e] = __int_as_float(c.x) - m;
-                js[put + e] = c.y;
-            }
-            put += n;
-        }
-    }
     // entry i of all warps' runs in order: which of them lie where depends on the raw counts, but
     // not the sequence of entries, so sums over i are the same from call to call
     int ends[kSolveWarps], from[kSolveWarps];
@@ -694,7 +770,7 @@ __global__ void __launch_bounds__(kSolveThreads) kv4_solve_kernel(const Kv4Args 
         return f + i;
     };
     const int all = close_up(mine);
-    if (direct) total = all;
+    if (fits) total = all;
 
     // ---- tau - m
     const float gamma = a.gamma;
@@ -716,7 +792,8 @@ __global__ void __launch_bounds__(kSolveThreads) kv4_solve_kernel(const Kv4Args 
         } else {
             for (int i = c0; i < c1; ++i) {
                 const int n = cn[i];
-                for (int e = lane; e < n; e += 32) add(__int_as_float(cand[(size_t)i * a.cap + e].x) - m);
+                const int2* list = list_of(i);
+                for (int e = lane; e < n; e += 32) add(__int_as_float(list[e].x) - m);
             }
         }
         F0 = warp_sum(F0); F1 = warp_sum(F1); F2 = warp_sum(F2);
@@ -794,15 +871,36 @@ __global__ void __launch_bounds__(kSolveThreads) kv4_solve_kernel(const Kv4Args 
             for (int u = 0; u < U; ++u) weigh(p[u], w[u], mt[u]);
         }
     } else {
+        // 32 candidates at a time: each lane its weight, then the warp's key slots take those that
+        // have one, four rounds of loads in flight
         for (int i = c0; i < c1; ++i) {
             const int n = cn[i];
-            for (int e = slot; e < n; e += KPW) {
-                const int2 c = cand[(size_t)i * a.cap + e];
-                const float p = entmax_p<GM>(__int_as_float(c.x) - m - sv.tau, gamma);
-                if (!(p > 0.f)) continue;
-                uint32_t w, mt;
-                fetch(c.y, w, mt);
-                weigh(p, w, mt);
+            const int2* list = list_of(i);
+            for (int b0 = 0; b0 < n; b0 += 32) {
+                const int2 c = b0 + lane < n ? list[b0 + lane] : make_int2(0, 0);
+                const float pl = b0 + lane < n ? entmax_p<GM>(__int_as_float(c.x) - m - sv.tau, gamma) : 0.f;
+                unsigned left = __ballot_sync(kFull, pl > 0.f);
+                while (left) {
+                    constexpr int U = 4;
+                    float p[U];
+                    uint32_t w[U], mt[U];
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        const int from = __fns(left, 0, slot + 1);   // the slot's bit of what is left (-1: none)
+                        const float pu = __shfl_sync(kFull, pl, from & 31);
+                        const int ju = __shfl_sync(kFull, c.y, from & 31);
+                        p[u] = 0.f;
+                        w[u] = mt[u] = 0u;
+                        if (from >= 0 && from < 32) {
+                            p[u] = pu;
+                            fetch(ju, w[u], mt[u]);
+                        }
+#pragma unroll
+                        for (int k = 0; k < KPW; ++k) left &= left - 1u;
+                    }
+#pragma unroll
+                    for (int u = 0; u < U; ++u) weigh(p[u], w[u], mt[u]);
+                }
             }
         }
     }
@@ -838,9 +936,7 @@ cudaError_t write_or_read(const Kv4Args& a, bool write, cudaStream_t s) {
 
 template <typename T, int D, int R>
 cudaError_t launch_scores(const Kv4Args& a, cudaStream_t s) {
-    const int rows = a.g.L * a.group;
-    const dim3 grid((a.nsplit + kScoreWarps - 1) / kScoreWarps, (rows + R - 1) / R, a.g.B * a.Hkv);
-    kv4_scores_kernel<T, D, R><<<grid, kScoreThreads, 0, s>>>(a);
+    kv4_scores_kernel<T, D, R><<<dim3(a.ctas, (a.g.B + a.seqs - 1) / a.seqs), kScoreThreads, 0, s>>>(a);
     return cudaGetLastError();
 }
 
@@ -857,19 +953,20 @@ cudaError_t attn(const Kv4Args& a, int gm, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.g.B * a.Hkv * a.g.L * a.group));
     cfg.blockDim = dim3(kSolveThreads);
+    cfg.dynamicSmemBytes = (size_t)(2 * kCap + 2 * a.nslot + 1) * 4;
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    switch (gm) {
-        case 1: return cudaLaunchKernelEx(&cfg, kv4_solve_kernel<T, D, 1>, a);
-        case 2: return cudaLaunchKernelEx(&cfg, kv4_solve_kernel<T, D, 2>, a);
-        case 3: return cudaLaunchKernelEx(&cfg, kv4_solve_kernel<T, D, 3>, a);
-        case 4: return cudaLaunchKernelEx(&cfg, kv4_solve_kernel<T, D, 4>, a);
-        default: return cudaLaunchKernelEx(&cfg, kv4_solve_kernel<T, D, 0>, a);
+    auto kern = gm == 1 ? kv4_solve_kernel<T, D, 1> : gm == 2 ? kv4_solve_kernel<T, D, 2>
+              : gm == 3 ? kv4_solve_kernel<T, D, 3> : gm == 4 ? kv4_solve_kernel<T, D, 4> : kv4_solve_kernel<T, D, 0>;
+    if (cfg.dynamicSmemBytes > 40 * 1024) {   // (beside up to 5 KB of static shared memory)
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes);
+        if (e != cudaSuccess) return e;
     }
+    return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
 }  // namespace
