@@ -24,6 +24,13 @@ constexpr unsigned kFull = 0xffffffffu;
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
+// the larger, or NaN where either is
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 __device__ __forceinline__ Kv4Seq seq_of(const Kv4Args& a, int b) {
     return kv4_seq(a.g, a.start[b], a.new_lens ? a.new_lens[b] : a.g.L);
 }
@@ -53,118 +60,194 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float* x) {
     *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// What the copying kernels share: blockIdx.y is the sequence and head, z 0 for keys, 1 for
+// values; a CTA takes kCopyRows * (256 / (D/8)) consecutive rows of the L, a thread the same
+// 8-value part of kCopyRows of them, so that their loads are in flight together (one row a
+// thread keeps 20 KB of reads in flight on an SM, a third of what the memory's latency asks).
+constexpr int kCopyRows = 4;
+template <int D>
+struct RowParts {
+    static constexpr int kParts = D / 8, kStep = kKvThreads / kParts, kRows = kCopyRows * kStep;
+    int b, h, l0, grp, c;   // sequence, head, first row; the part's group of 32 dimensions and quarter
+    int page[kCopyRows];    // of each row; -1: the row is padding, -2: its page is not in the pool
+    Kv4Seq s;
+    size_t at0;             // element offset of the part of row l0 in [B][Hkv][L][D]
+    __device__ __forceinline__ explicit RowParts(const Kv4Args& a) {
+        const int bh = blockIdx.y, t = threadIdx.x % kParts;
+        b = bh / a.Hkv;
+        h = bh - b * a.Hkv;
+        l0 = blockIdx.x * kRows + threadIdx.x / kParts;
+        grp = t >> 2;
+        c = t & 3;
+        at0 = ((size_t)bh * a.g.L + l0) * D + t * 8;
+        s = seq_of(a, b);
+        if (s.bad && a.bad && l0 == 0 && t == 0) atomicOr(a.bad, s.bad);
+        const int* table = a.table + (size_t)b * a.g.max_pages;
+#pragma unroll
+        for (int u = 0; u < kCopyRows; ++u) {
+            page[u] = -1;
+            if (l(u) < s.rows) {
+                page[u] = kv4_page(a.g, table, s.start + l(u));
+                if (page[u] < 0) {
+                    page[u] = -2;
+                    if (a.bad && t == 0) atomicOr(a.bad, kKvBadPage);
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ int l(int u) const { return l0 + u * kStep; }
+    __device__ __forceinline__ size_t at(int u) const { return at0 + (size_t)u * kStep * D; }
+};
+
 // ------------------------------------------------------------------ write
-// Four threads per group of 32 dimensions, 8 each; blockIdx.y: 0 keys, 1 values.
+// Four threads per group of 32 dimensions, 8 each.
 //     zero = bf16(min),  scale = bf16((max - zero) / 15),  code = rint((x - zero) / scale)
-// as they are in 64-bit arithmetic, so that the codes do not depend on who computes them:
-// the pair is computed in double by the group's threads, and an element's code in float
-// where its quotient is clear of a half-integer, in double where it is not (float's
-// quotient is within 2^-22 of it relative, at most 4e-6 for one up to 15.1; the few
-// elements nearer than 1e-4 to a tie, exact ties among them, take the division again).
+// as they are in 64-bit arithmetic, so that the codes do not depend on who computes them.
+// Float gets there but for values next to a border: its scale is within 2^-21 of the exact
+// one, so only a quotient that near to the middle of two bf16 numbers can round otherwise;
+// and its quotient of an element is off by at most 4e-6 (2^-22 of at most 15.1).  Where the
+// scale lies within 8 float steps (2^-20) of a middle it is computed in double.  An element
+// within 1e-4 of a half-integer h -- exact ties are common, 0.2 % of bf16 elements -- is
+// decided by the sign of (x - z) - scale h: the difference is carried exactly as t + e (the
+// error-free sum), scale h has 13 bits, and t - scale h is exact that near to zero.
 // A group with a NaN, an infinity, or a minimum that rounds to one is stored as (0, NaN):
 // it reads back as NaN.
+// Bound by memory at long prompts: 256 + 80 bytes a row of 128 bf16 values.
 template <typename T, int D>
 __global__ void __launch_bounds__(kKvThreads) kv4_write_kernel(const Kv4Args a) {
-    constexpr int TPR = D / 8, G = D / kKvGroup;
-    const T* src = static_cast<const T*>(blockIdx.y ? a.v : a.k);
-    uint32_t* codes = reinterpret_cast<uint32_t*>(blockIdx.y ? a.v_codes : a.k_codes);
-    uint32_t* meta = reinterpret_cast<uint32_t*>(blockIdx.y ? a.v_meta : a.k_meta);
-    const long long item = (long long)blockIdx.x * kKvThreads + threadIdx.x;
-    const long long row = item / TPR;   // (b * Hkv + h) * L + l
-    const int t = (int)(item % TPR);
-    if (row >= (long long)a.g.B * a.Hkv * a.g.L) return;   // whole quads leave together
-    const int l = (int)(row % a.g.L);
-    const int bh = (int)(row / a.g.L), b = bh / a.Hkv, h = bh - b * a.Hkv;
-    const Kv4Seq s = seq_of(a, b);
-    if (s.bad && a.bad && l == 0 && t == 0) atomicOr(a.bad, s.bad);
-    if (l >= s.rows) return;
-    const int pos = s.start + l;
-    const int page = kv4_page(a.g, a.table + (size_t)b * a.g.max_pages, pos);
-    if (page < 0) {
-        if (a.bad && t == 0) atomicOr(a.bad, kKvBadPage);
-        return;
-    }
-    const unsigned quad = 0xfu << (threadIdx.x & 28);
-    float x[8];
-    load8(src + row * D + t * 8, x);
-    float lo = x[0], hi = x[0];
-    bool fine = isfinite(x[0]);
+    constexpr int G = D / kKvGroup;
+    const RowParts<D> p(a);
+    const unsigned quad = 0xfu << (threadIdx.x & 28);   // (rows are whole quads)
+    const T* src = static_cast<const T*>(blockIdx.z ? a.v : a.k);
+    float xs[kCopyRows][8];
+#pragma unroll
+    for (int u = 0; u < kCopyRows; ++u)
+        if (p.l(u) < p.s.rows) load8(src + p.at(u), xs[u]);
+#pragma unroll
+    for (int u = 0; u < kCopyRows; ++u) {
+    if (p.page[u] < 0) continue;
+    const float (&x)[8] = xs[u];
+    // (a NaN passes through max_nan; lo is only used where hi, and so every value, is fine)
+    float lo = x[0], hi = x[0], big = fabsf(x[0]);
 #pragma unroll
     for (int i = 1; i < 8; ++i) {
         lo = fminf(lo, x[i]);
         hi = fmaxf(hi, x[i]);
-        fine &= isfinite(x[i]);
+        big = max_nan(big, fabsf(x[i]));
     }
 #pragma unroll
     for (int o = 1; o < 4; o <<= 1) {
         lo = fminf(lo, __shfl_xor_sync(quad, lo, o));
         hi = fmaxf(hi, __shfl_xor_sync(quad, hi, o));
-        fine &= __shfl_xor_sync(quad, (int)fine, o) != 0;
+        big = max_nan(big, __shfl_xor_sync(quad, big, o));
     }
     const __nv_bfloat16 zb = __float2bfloat16_rn(lo);
     const float z = __bfloat162float(zb);
-    fine &= isfinite(z);
-    const double range = (double)hi - (double)z;
-    const __nv_bfloat16 sb = __float2bfloat16_rn(fine && range > 0. ? (float)(range / 15.) : 0.f);
+    const bool fine = big < INFINITY && fabsf(z) < INFINITY;
+    float sq = (hi - z) * (1.f / 15.f);
+    const int low = (int)(__float_as_uint(sq) & 0xffffu) - 0x8000;
+    if (!(sq > 1e-30f && sq < 1e30f) || (low > -8 && low < 8)) {
+        const double range = (double)hi - (double)z;
+        sq = range > 0. ? (float)(range / 15.) : 0.f;
+    }
+    const __nv_bfloat16 sb = __float2bfloat16_rn(fine ? sq : 0.f);
     const float sc = __bfloat162float(sb);
     uint32_t w = 0;
     if (sc > 0.f) {
         const float inv = 1.f / sc;
+        constexpr float kRound = 12582912.f;   // 1.5 * 2^23: adding it rounds to an integer
+        float near = 0.f;                      // largest distance from the integer taken
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            float qv = (x[i] - z) * inv;   // (an underflowing or overflowing inverse is caught below)
-            float r = rintf(qv);
-            if (!(fabsf(fabsf(qv - r) - 0.5f) > 1e-4f) || !(inv >= 1e-30f && inv <= 1e30f)) {
-                const double qd = ((double)x[i] - (double)z) / (double)sc;
-                r = (float)rint(qd);
+            const float q = fminf(fmaxf((x[i] - z) * inv, 0.f), 15.f);
+            const float y = q + kRound;
+            near = max_nan(near, fabsf(q - (y - kRound)));
+            w += (__float_as_uint(y) & 15u) << (4 * i);
+        }
+        if (!(inv >= 1e-30f && inv <= 1e30f)) {
+            w = 0;
+#pragma unroll 1
+            for (int i = 0; i < 8; ++i) {
+                float xi = x[0];
+#pragma unroll
+                for (int k = 1; k < 8; ++k) xi = k == i ? x[k] : xi;
+                const double q = rint(((double)xi - (double)z) / (double)sc);
+                w |= (uint32_t)(int)fmin(fmax(q, 0.), 15.) << (4 * i);
             }
-            w |= (uint32_t)fminf(fmaxf(r, 0.f), 15.f) << (4 * i);
+        } else if (near >= 0.4999f) {
+            w = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float t = x[i] - z, bb = t - x[i], e = (x[i] - (t - bb)) - (z + bb);
+                const float q = fminf(fmaxf(t * inv, 0.f), 15.f);
+                const float n = truncf(q), h = n + 0.5f;
+                uint32_t code = (uint32_t)(int)rintf(q);
+                if (fabsf(q - h) < 2e-4f) {
+                    const float d = (t - sc * h) + e;
+                    const uint32_t down = (uint32_t)(int)n;
+                    code = d > 0.f ? down + 1 : d < 0.f ? down : down + (down & 1u);
+                }
+                w |= code << (4 * i);
+            }
         }
     }
-    const size_t at = kv4_row(a.g, a.Hkv, page, h, pos);
-    const int grp = t >> 2, c = t & 3;
-    codes[at * (D / 8) + c * G + grp] = w;
-    if (c == 0) {
+    const size_t at = kv4_row(a.g, a.Hkv, p.page[u], p.h, p.s.start + p.l(u));
+    reinterpret_cast<uint32_t*>(blockIdx.z ? a.v_codes : a.k_codes)[at * (D / 8) + p.c * G + p.grp] = w;
+    if (p.c == 0) {
         const uint32_t zw = fine ? (uint32_t)__bfloat16_as_ushort(zb) : 0x7fffu;
-        meta[at * G + grp] = (uint32_t)__bfloat16_as_ushort(sb) | zw << 16;
+        reinterpret_cast<uint32_t*>(blockIdx.z ? a.v_meta : a.k_meta)[at * G + p.grp] =
+            (uint32_t)__bfloat16_as_ushort(sb) | zw << 16;
     }
+    }   // rows
 }
 
 // ------------------------------------------------------------------ read
 // A thread per word of codes: 8 values zero + scale * code (one fused multiply-add each:
-// exact but for the last rounding).  Rows past new_lens, and rows of a page outside the
-// pool, are zeros.
+// exact but for the last rounding).  A nibble under the bits of 2^23 is the float 2^23 +
+// 16^i code: the first five need no shift, and the scale carries the 16^-i.
+// Rows past new_lens, and rows of a page outside the pool, are zeros.
 template <typename T, int D>
 __global__ void __launch_bounds__(kKvThreads) kv4_read_kernel(const Kv4Args a) {
-    constexpr int TPR = D / 8, G = D / kKvGroup;
-    T* dst = static_cast<T*>(blockIdx.y ? a.v_out : a.k_out);
-    const uint32_t* codes = reinterpret_cast<const uint32_t*>(blockIdx.y ? a.v_codes : a.k_codes);
-    const uint32_t* meta = reinterpret_cast<const uint32_t*>(blockIdx.y ? a.v_meta : a.k_meta);
-    const long long item = (long long)blockIdx.x * kKvThreads + threadIdx.x;
-    const long long row = item / TPR;
-    const int t = (int)(item % TPR);
-    if (row >= (long long)a.g.B * a.Hkv * a.g.L) return;
-    const int l = (int)(row % a.g.L);
-    const int bh = (int)(row / a.g.L), b = bh / a.Hkv, h = bh - b * a.Hkv;
-    const Kv4Seq s = seq_of(a, b);
-    if (s.bad && a.bad && l == 0 && t == 0) atomicOr(a.bad, s.bad);
-    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    const int grp = t >> 2, c = t & 3;
-    if (l < s.rows) {
-        const int pos = s.start + l;
-        const int page = kv4_page(a.g, a.table + (size_t)b * a.g.max_pages, pos);
-        if (page >= 0) {
-            const size_t at = kv4_row(a.g, a.Hkv, page, h, pos);
-            const uint32_t w = codes[at * (D / 8) + c * G + grp];
-            const uint32_t m = meta[at * G + grp];
-            const float sc = bf16_lo(m), z = bf16_hi(m);
+    constexpr int G = D / kKvGroup;
+    const RowParts<D> p(a);
+    const uint32_t* codes = reinterpret_cast<const uint32_t*>(blockIdx.z ? a.v_codes : a.k_codes);
+    const uint32_t* meta = reinterpret_cast<const uint32_t*>(blockIdx.z ? a.v_meta : a.k_meta);
+    T* dst = static_cast<T*>(blockIdx.z ? a.v_out : a.k_out);
+    uint32_t w[kCopyRows], m[kCopyRows];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = fmaf(sc, (float)((w >> (4 * i)) & 15u), z);
-        } else if (a.bad && t == 0) {
-            atomicOr(a.bad, kKvBadPage);
+    for (int u = 0; u < kCopyRows; ++u) {
+        w[u] = m[u] = 0u;   // zeros
+        if (p.page[u] >= 0) {
+            const size_t at = kv4_row(a.g, a.Hkv, p.page[u], p.h, p.s.start + p.l(u));
+            w[u] = __ldg(codes + at * (D / 8) + p.c * G + p.grp);
+            m[u] = __ldg(meta + at * G + p.grp);
         }
     }
-    store8(dst + row * D + t * 8, x);
+#pragma unroll
+    for (int u = 0; u < kCopyRows; ++u) {
+        if (p.l(u) >= a.g.L) break;
+        const float sc = bf16_lo(m[u]), z = bf16_hi(m[u]);
+        float x[8];
+        // (a scale below 2^-106 would lose bits to the 16^-4: it takes the codes themselves)
+        if (sc > 1e-31f) {
+            float f = sc;
+#pragma unroll
+            for (int i = 0; i < 5; ++i) {
+                x[i] = fmaf(f, __uint_as_float((w[u] & (15u << (4 * i))) | 0x4b000000u) - 8388608.f, z);
+                f *= 0.0625f;
+            }
+            f = sc;
+#pragma unroll
+            for (int i = 0; i < 3; ++i) {
+                x[5 + i] = fmaf(f, __uint_as_float((w[u] >> 20 & (15u << (4 * i))) | 0x4b000000u) - 8388608.f, z);
+                f *= 0.0625f;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = fmaf(sc, (float)((w[u] >> (4 * i)) & 15u), z);
+        }
+        store8(dst + p.at(u), x);
+    }
 }
 
 // ------------------------------------------------------------------ scores
@@ -214,12 +297,6 @@ __device__ __forceinline__ void mma_1688_bf(float (&c)[4], uint32_t a0, uint32_t
 __device__ __forceinline__ uint32_t pack_half(float a, float b) {
     const __half2 h = __floats2half2_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&h);
-}
-// the larger, or NaN where either is
-__device__ __forceinline__ float max_nan(float a, float b) {
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
 }
 // x rounded to bf16, in the upper half of a word; what is left stays in x
 __device__ __forceinline__ uint32_t bf16_part(float& x) {
@@ -927,8 +1004,8 @@ __global__ void __launch_bounds__(kSolveThreads) kv4_solve_kernel(const Kv4Args 
 // ------------------------------------------------------------------ launches
 template <typename T, int D>
 cudaError_t write_or_read(const Kv4Args& a, bool write, cudaStream_t s) {
-    const long long items = (long long)a.g.B * a.Hkv * a.g.L * (D / 8);
-    const dim3 grid((unsigned)((items + kKvThreads - 1) / kKvThreads), 2);
+    constexpr int rows = RowParts<D>::kRows;
+    const dim3 grid((a.g.L + rows - 1) / rows, a.g.B * a.Hkv, 2);
     if (write) kv4_write_kernel<T, D><<<grid, kKvThreads, 0, s>>>(a);
     else kv4_read_kernel<T, D><<<grid, kKvThreads, 0, s>>>(a);
     return cudaGetLastError();
