@@ -6,6 +6,8 @@ contiguous, float32 or bfloat16, on one CUDA device.
 """
 from __future__ import annotations
 
+import contextlib
+
 import torch
 
 from . import capi
@@ -18,9 +20,14 @@ def _stream_handle(device) -> int:
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 
-# The library launches on the calling thread's current CUDA device; every call below
-# runs with the tensors' device made current, so tensors on another GPU than the
-# current one are handled on theirs.
+_SAME_DEVICE = contextlib.nullcontext()
+
+
+def _on(device):
+    """The library launches on the calling thread's current CUDA device; every call below
+    runs with the tensors' device made current, so tensors on another GPU than the
+    current one are handled on theirs."""
+    return _SAME_DEVICE if device.index == torch._C._cuda_getDevice() else torch.cuda.device(device)
 
 
 def _check(*ts):
@@ -104,7 +111,7 @@ def entmax_attn_fwd(q, k, v, alpha: float = 1.5, causal: bool = False, *, with_i
         if otilde is not None:
             _check_otilde(otilde, q)
         big = 2 ** 31 - 1
-        with torch.cuda.device(q.device):
+        with _on(q.device):
             st = capi.ent_attn_fwd_window(*args[:9], min(window, big), min(sinks, big), *args[10:],
                                           otilde.data_ptr() if otilde is not None else None, *tail)
         _raise(st, "ent_attn_fwd_window")
@@ -112,16 +119,16 @@ def entmax_attn_fwd(q, k, v, alpha: float = 1.5, causal: bool = False, *, with_i
         if otilde is not None:
             raise ValueError("otilde and lists are separate forward variants")
         lk, lu, ln = lists
-        with torch.cuda.device(q.device):
+        with _on(q.device):
             st = capi.ent_attn_fwd_lists(*args, lk.data_ptr(), lu.data_ptr(), ln.data_ptr(), *tail)
         _raise(st, "ent_attn_fwd_lists")
     elif otilde is None:
-        with torch.cuda.device(q.device):
+        with _on(q.device):
             st = capi.ent_attn_fwd(*args, *tail)
         _raise(st, "ent_attn_fwd")
     else:
         _check_otilde(otilde, q)
-        with torch.cuda.device(q.device):
+        with _on(q.device):
             st = capi.ent_attn_fwd_otilde(*args, otilde.data_ptr(), *tail)
         _raise(st, "ent_attn_fwd_otilde")
     return o, tau, mask, iters
@@ -162,7 +169,7 @@ def entmax_attn_bwd(q, k, v, o, dout, tau, block_mask, alpha: float = 1.5, causa
         if otilde is not None:
             _check_otilde(otilde, q)
         big = 2 ** 31 - 1
-        with torch.cuda.device(q.device):
+        with _on(q.device):
             st = capi.ent_attn_bwd_window(q.data_ptr(), k.data_ptr(), v.data_ptr(),
                                           otilde.data_ptr() if otilde is not None else None,
                                           *tail[:9], min(window, big), min(sinks, big), *tail[10:])
@@ -171,18 +178,18 @@ def entmax_attn_bwd(q, k, v, o, dout, tau, block_mask, alpha: float = 1.5, causa
         if otilde is not None:
             raise ValueError("otilde and lists are separate backward variants")
         lk, lu, ln = lists
-        with torch.cuda.device(q.device):
+        with _on(q.device):
             st = capi.ent_attn_bwd_lists(q.data_ptr(), k.data_ptr(), v.data_ptr(), lk.data_ptr(),
                                          lu.data_ptr(), ln.data_ptr(), *tail)
         _raise(st, "ent_attn_bwd_lists")
     elif otilde is None:
-        with torch.cuda.device(q.device):
+        with _on(q.device):
             st = capi.ent_attn_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(),
                                    o.data_ptr() if o is not None else None, *tail)
         _raise(st, "ent_attn_bwd")
     else:
         _check_otilde(otilde, q)
-        with torch.cuda.device(q.device):
+        with _on(q.device):
             st = capi.ent_attn_bwd_otilde(q.data_ptr(), k.data_ptr(), v.data_ptr(),
                                           otilde.data_ptr(), *tail)
         _raise(st, "ent_attn_bwd_otilde")
@@ -191,7 +198,7 @@ def entmax_attn_bwd(q, k, v, o, dout, tau, block_mask, alpha: float = 1.5, causa
 
 def read_status(ws: torch.Tensor) -> list[int]:
     """Counters of the last call that used ``ws`` (synchronises); raises on a timeout flag."""
-    with torch.cuda.device(ws.device):
+    with _on(ws.device):
         st, ctr = capi.ent_attn_read_status(ws.data_ptr(), _stream_handle(ws.device))
     _raise(st, "ent_attn_read_status")
     return ctr
@@ -271,7 +278,7 @@ def entmax_rows_fwd(z, alpha: float = 1.5, solver: str = "hist", *, out=None):
         iters = torch.empty(rows, dtype=torch.uint8, device=z.device)
     else:
         p, tau, iters = out
-    with torch.cuda.device(z.device):
+    with _on(z.device):
         st = capi.ent_entmax_rows_fwd(z.data_ptr(), rows, n, _DTYPES[z.dtype], alpha,
                                       SOLVERS[solver], p.data_ptr(), tau.data_ptr(),
                                       iters.data_ptr() if iters is not None else None,
@@ -285,7 +292,7 @@ def entmax_rows_bwd(z, tau, dp, alpha: float = 1.5, *, out=None):
     _check_rows(z, dp)
     rows, n = z.shape
     dz = torch.empty_like(z) if out is None else out
-    with torch.cuda.device(z.device):
+    with _on(z.device):
         st = capi.ent_entmax_rows_bwd(z.data_ptr(), tau.data_ptr(), dp.data_ptr(), rows, n,
                                       _DTYPES[z.dtype], alpha, dz.data_ptr(),
                                       _stream_handle(z.device))

@@ -54,6 +54,15 @@ struct WinBlocks {
     __host__ __device__ __forceinline__ bool has(int b) const { return b < ns || b >= w0; }
 };
 
+// Bits 0 .. n-1 of 64.
+__device__ __forceinline__ unsigned long long low_bits(int n) {
+    return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1ull;
+}
+// Columns 0 .. 63 from key key0 on that query i sees, nv of which are admissible at all.
+__device__ __forceinline__ unsigned long long win_cols64(int window, int sinks, int i, int key0, int nv) {
+    return low_bits(nv) & (~low_bits(i - window + 1 - key0) | low_bits(sinks - key0));
+}
+
 // Keys that query i sees.
 __host__ __device__ __forceinline__ int win_keys(int window, int sinks, int i) {
     if (i < window) return i + 1;

@@ -279,7 +279,8 @@ ent_status fwd_impl(const void* q, const void* k, const void* v, int B, int H, i
     const FwdLayout FL = fwd_layout(B, H, N, d);
     // (no tile of a shorter sequence runs the bound pass, so its statistics are not computed)
     // (nor under a window, whose tiles visit few blocks: there the histogram start, the bound
-    // pass and the calibrated start are all off)
+    // pass and the calibrated start are all off; a start calibrated on windowed rows left the
+    // forward's time as it was, 432 us on B8 H12 N2048 d64 window 512, and cost 23 us)
     const bool bound = dtype == ENT_BF16 && hist_budget() == 0 && bound_enabled() && !empty &&
                        !win.want && n_tiles(N) >= ent::kBoundMinBlocks;
     // header, failure list (entries are tile + 1, 0 until written) and the per-head max |c|
@@ -328,7 +329,8 @@ ent_status fwd_impl(const void* q, const void* k, const void* v, int B, int H, i
         a.cent = base + FL.cent;
     }
     if (dtype == ENT_F32) {
-        e = ent::simt_fwd_f32(a, d, gm, s);
+        e = win.want && ent::win_f32_fits(a.window, a.sinks, d) ? ent::win_fwd_f32(a, d, gm, s)
+                                                                : ent::simt_fwd_f32(a, d, gm, s);
     } else {
         const char* why = nullptr;
         e = ent::tc_fwd(a, d, gm, s, &why);
@@ -398,7 +400,8 @@ ent_status bwd_impl(const void* q, const void* k, const void* v, const float* ot
         a.dv_acc = reinterpret_cast<float*>(base + LL.dv);
     }
     if (dtype == ENT_F32) {
-        e = ent::simt_bwd_f32(a, d, gm, s);
+        e = win.want && ent::win_f32_fits(a.window, a.sinks, d) ? ent::win_bwd_f32(a, d, gm, s)
+                                                                : ent::simt_bwd_f32(a, d, gm, s);
     } else {
         const char* why = nullptr;
         if (lists.want) {
@@ -733,14 +736,14 @@ ent_status check_kv4(ent::Kv4Args& a, const void* kc, const void* km, const void
     return ENT_OK;
 }
 
-// Workspace of the attention: the items' run counts (an item is a block of rows of one key
-// head), per row and run its maximum, its count and its first chunk, then the candidates
-// (score and key).  The rows of one key head share a scores warp, 4, 8, 16 or 32
-// of them (the product is 8 queries wide; a warp of 4 looks its scores through with twice the
-// lanes a row; float32 rows at d = 128 take two parts each and stay at 16).
+// Workspace of the attention: per row and run of chunks its maximum and its count, then the
+// candidates (score and key).  The rows of one key head share a scores warp, 4, 8, 16 or 32
+// of them (the product is 8 queries wide; a warp of 4 holds two groups of dimensions in it and
+// looks its scores through with twice the lanes a row; float32 rows at d = 128 take two parts
+// each and stay at 16).
 struct Kv4Layout {
-    int block, blocks, chunk, nchunk, nslot, ctas, seqs;
-    size_t max, n, at, cand, total;
+    int block, blocks, chunk, nchunk, nrun;
+    size_t n, cand, total;
 };
 
 bool kv4_layout(const ent::Kv4Geom& g, long long rows, int group, int d, int dtype, Kv4Layout* l) {
@@ -750,22 +753,15 @@ bool kv4_layout(const ent::Kv4Geom& g, long long rows, int group, int d, int dty
     l->blocks = (int)((per + l->block - 1) / l->block);
     l->chunk = ent::kv4_chunk_keys(l->block);
     l->nchunk = ent::kv4_chunks(g, l->chunk);
-    // one round of CTAs that stays: two on each SM, or one of the wide ones, shared out among
-    // the groups; no more than there are chunks for
-    const long long heads = per > 0 ? rows / per : 0;
-    const int groups = (g.B + ent::kKvSeqs - 1) / ent::kKvSeqs;
-    l->seqs = g.B < ent::kKvSeqs ? g.B : ent::kKvSeqs;
-    const long long chunks = groups > 0 ? heads * l->blocks * l->nchunk / groups + 1 : 1;
-    const int sms = l->block <= 8 ? 296 : 148;
-    long long want = (chunks / 2 + ent::kKvScoreWarps) / ent::kKvScoreWarps;
-    const int most = groups > 0 ? (sms + groups - 1) / groups : 1;
-    l->ctas = (int)(want < most ? want : most);
-    l->nslot = l->ctas * ent::kKvScoreWarps < l->nchunk ? l->ctas * ent::kKvScoreWarps : l->nchunk;
-    const size_t runs = (size_t)rows * l->nslot * 4;
-    l->max = round_up((size_t)heads * l->blocks * 4, 256);
-    l->n = l->max + round_up(runs, 256);
-    l->at = l->n + round_up(runs, 256);
-    l->cand = l->at + round_up(runs, 256);
+    // runs: a warp each, enough of them for two rounds of 16 on each SM and no more (a longer
+    // run pays its prologue once, and a higher maximum filters its later chunks)
+    const long long items = per > 0 ? rows / per * l->blocks : 0;
+    long long want = items > 0 ? (2 * 16 * 148 + items - 1) / items : 1;
+    if (want > ent::kKvMaxRuns) want = ent::kKvMaxRuns;
+    l->nrun = (int)(want < l->nchunk ? want : l->nchunk);
+    const size_t runs = (size_t)rows * l->nrun * 4;
+    l->n = round_up(runs, 256);
+    l->cand = l->n + round_up(runs, 256);
     l->total = l->cand + round_up((size_t)rows * l->nchunk * l->chunk * 8, 256);
     return true;
 }
@@ -860,13 +856,10 @@ ent_status ent_attn_kv4_fwd(const void* q, int B, int Hq, int Hkv, int L, int d,
     a.alpha = alpha;
     const int gm = gamma_mode(alpha, &a.gamma);
     a.cx = (alpha - 1.f) / sqrtf((float)d);
-    a.block = l.block; a.blocks = l.blocks; a.chunk = l.chunk; a.nchunk = l.nchunk;
-    a.nslot = l.nslot; a.ctas = l.ctas; a.seqs = l.seqs;
+    a.block = l.block; a.blocks = l.blocks; a.chunk = l.chunk; a.nchunk = l.nchunk; a.nrun = l.nrun;
     char* base = static_cast<char*>(ws);
-    a.item_n = reinterpret_cast<int*>(base);
-    a.run_max = reinterpret_cast<float*>(base + l.max);
+    a.run_max = reinterpret_cast<float*>(base);
     a.run_n = reinterpret_cast<int*>(base + l.n);
-    a.run_at = reinterpret_cast<int*>(base + l.at);
     a.cand = reinterpret_cast<int2*>(base + l.cand);
     cudaError_t e = ent::kv4_attn(a, d, dtype == ENT_BF16, gm, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? ENT_OK : cuda_fail(e, "cache attention launch");

@@ -141,18 +141,14 @@ struct Kv4Args {
     float alpha, gamma, cx;     // as in FwdArgs
     int block, blocks;          // query rows of a scores warp (4, 8, 16 or 32), such blocks of a key head
     int chunk, nchunk;          // keys of a chunk, most chunks of a sequence
-    int nslot;                  // most runs (a worker's share of an item) of an item
-    int ctas, seqs;             // scores CTAs a group of sequences, sequences a group
-    int* item_n;                // workspace: [B Hkv][blocks] runs of the item
-    float* run_max;             //            [rows][nslot], rows = B Hkv L group
-    int* run_n;                 //            [rows][nslot]
-    int* run_at;                //            [rows][nslot] first chunk
-    int2* cand;                 //            [rows][nchunk * chunk]: score bits, key; a run's from run_at on
+    int nrun;                   // runs of chunks of a sequence, a scores warp each
+    float* run_max;             // workspace: [rows][nrun], rows = B Hkv L group
+    int* run_n;                 //            [rows][nrun]
+    int2* cand;                 //            [rows][nchunk * chunk]: score bits, key; a run's from its
+                                //            first chunk's place on
 };
 __host__ __device__ constexpr int kv4_chunk_keys(int block) { return block == 32 ? 32 : 64; }
-constexpr int kKvSeqs = 256;          // sequences of a group (one thread each)
-constexpr int kKvScoreWarps = 8;      // warps of a scores CTA
-constexpr int kKvMaxRuns = 296 * kKvScoreWarps;
+constexpr int kKvMaxRuns = 1024;
 cudaError_t kv4_write(const Kv4Args& a, int d, bool bf16, cudaStream_t s);
 cudaError_t kv4_read(const Kv4Args& a, int d, bool bf16, cudaStream_t s);
 cudaError_t kv4_attn(const Kv4Args& a, int d, bool bf16, int gm, cudaStream_t s);
@@ -160,6 +156,12 @@ cudaError_t kv4_attn(const Kv4Args& a, int d, bool bf16, int gm, cudaStream_t s)
 // FP32 CUDA-core path: float32 inputs (scores by FFMA, no TF32 rounding).
 cudaError_t simt_fwd_f32(const FwdArgs& a, int d, int gm, cudaStream_t s);
 cudaError_t simt_bwd_f32(const BwdArgs& a, int d, int gm, cudaStream_t s);
+
+// float32 under a window whose scores fit in shared memory (win_f32.cu); the others take the
+// general kernels above.
+bool win_f32_fits(int window, int sinks, int d);
+cudaError_t win_fwd_f32(const FwdArgs& a, int d, int gm, cudaStream_t s);
+cudaError_t win_bwd_f32(const BwdArgs& a, int d, int gm, cudaStream_t s);
 
 // bf16 tensor-core path (tcgen05 + TMEM + TMA).  `why` names a host-side failure.
 cudaError_t tc_fwd(const FwdArgs& a, int d, int gm, cudaStream_t s, const char** why);

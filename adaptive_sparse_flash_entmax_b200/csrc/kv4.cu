@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(kKvThreads) kv4_read_kernel(const Kv4Args a) {
 }
 
 // ------------------------------------------------------------------ scores
-// A warp per (run of chunks of C keys, block of R rows, sequence and key head); the eight warps
+// A warp per (run of chunks of C keys, block of R rows, sequence and key head); the four warps
 // of a CTA share nothing but the rows' maxima so far.  The rows are the new tokens' queries of all heads that share the
 // key head, row = l * group + head of the group.  Keys are the M = 16 rows of an m16n8k16
 // product and the queries its 8 columns; the contraction index is permuted so that a lane's
@@ -319,80 +319,41 @@ __device__ __forceinline__ void load_words(const uint32_t* p, uint32_t (&w)[G]) 
     }
 }
 
-constexpr int kScoreWarps = kKvScoreWarps;
+constexpr int kScoreWarps = 4;
 constexpr int kScoreThreads = kScoreWarps * 32;
-static_assert(kScoreThreads == kKvSeqs, "a thread per sequence of the group");
 
 // R: rows of a block (4, 8, 16 or 32), in NT products of 8 columns.
 template <typename T, int D, int R>
-__global__ void __launch_bounds__(kScoreThreads, R <= 8 ? 2 : 1) kv4_scores_kernel(const Kv4Args a) {
+__global__ void __launch_bounds__(kScoreThreads, R == 4 ? 5 : R == 8 ? 4 : 2) kv4_scores_kernel(const Kv4Args a) {
     constexpr int G = D / kKvGroup, NT = R <= 8 ? 1 : R / 8, C = kv4_chunk_keys(R), U = C / kKvTile;
     constexpr int LPR = 32 / R, KPL = C / LPR;   // lanes a row, keys a lane
     constexpr int kStride = C + 4;   // spreads a product's 8 keys x 4 row pairs over the banks
     constexpr bool F32 = sizeof(T) == 4;
     __shared__ __align__(16) float xs_all[kScoreWarps][8 * NT * kStride];
-    __shared__ unsigned long long pub[kScoreWarps][R];   // item << 32 | the row's maximum so far
-    __shared__ long long pre[kKvSeqs + 1];               // chunks of the group before each sequence
-    __shared__ long long warp_sum[kScoreWarps];
+    // With four rows the product's 8 columns hold two groups of dimensions, h and h + G/2, each
+    // MMA half of its contraction over either: columns 0-3 are the rows with the first group,
+    // 4-7 with the second.  As many products, but half the scale multiplications.
+    constexpr bool PAIR = R == 4 && G >= 2;
+    constexpr int GS = PAIR ? G / 2 : G;         // groups that a lane scales
+    __shared__ float row_max[R];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     float* xs = xs_all[warp];
-
-    // ---- the group's work, and this warp's share of it
-    const int b0 = blockIdx.y * a.seqs, nseq = kv4_min(a.seqs, a.g.B - b0);
-    {
-        const int i = threadIdx.x;
-        long long n = 0;
-        if (i < nseq) {
-            const Kv4Seq s = seq_of(a, b0 + i);
-            if (s.bad && a.bad && blockIdx.x == 0) atomicOr(a.bad, s.bad);
-            if (s.rows > 0)
-                n = (long long)kv4_seq_chunks(a.g, s, C) * a.Hkv * ((s.rows * a.group + R - 1) / R);
-        }
-        long long incl = n;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long y = __shfl_up_sync(kFull, incl, o);
-            if (lane >= o) incl += y;
-        }
-        if (lane == 31) warp_sum[warp] = incl;
-        if (lane < R) pub[warp][lane] = ~0ull;
-        __syncthreads();
-        for (int w = 0; w < warp; ++w) incl += warp_sum[w];
-        pre[i + 1] = incl;
-        if (i == 0) pre[0] = 0;
-        __syncthreads();
-    }
-    const long long T_all = pre[nseq];
-    const int W = kv4_workers(T_all, gridDim.x * kScoreWarps), worker = blockIdx.x * kScoreWarps + warp;
-    if (worker >= W) return;
-    long long x0 = kv4_share(T_all, W, worker);
-    const long long x1 = kv4_share(T_all, W, worker + 1);
+    const int bk = blockIdx.z, b = bk / a.Hkv, hk = bk - b * a.Hkv;
+    const Kv4Seq s = seq_of(a, b);
+    if (s.bad && a.bad && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(a.bad, s.bad);
+    const int row0 = blockIdx.y * R, nrows = s.rows * a.group;   // real rows of this key head
+    const int nch = kv4_seq_chunks(a.g, s, C), run = kv4_run(nch, a.nrun);
+    const int slot = blockIdx.x * kScoreWarps + warp;
+    const int ch0 = slot * run, ch1 = kv4_min(ch0 + run, nch);
+    if (threadIdx.x < R) row_max[threadIdx.x] = -INFINITY;
+    __syncthreads();
+    if (row0 >= nrows || ch0 >= ch1) return;   // (the solver takes no more runs than hold a chunk)
 
     const int c = lane & 3, key = lane >> 2;   // the lane's keys of a tile: key and key + 8
     const int lrow = lane / LPR, sub = lane % LPR;   // the row that it looks through, and its part of it
     constexpr int kTokenB = D / 2, kMetaB = 4 * G;   // bytes of a token
     const size_t page_rows = (size_t)a.Hkv << a.g.page_shift;
     const int mask = (1 << a.g.page_shift) - 1;
-
-#pragma unroll 1
-    while (x0 < x1) {
-    // ---- the item that chunk x0 belongs to, and the run of it that is this warp's
-    int i = 0;
-#pragma unroll
-    for (int step = kKvSeqs / 2; step > 0; step >>= 1)
-        if (i + step < nseq && pre[i + step] <= x0) i += step;
-    const int b = b0 + i;
-    const Kv4Seq s = seq_of(a, b);
-    const int nrows = s.rows * a.group, nch = kv4_seq_chunks(a.g, s, C), nblk = (nrows + R - 1) / R;
-    const long long rem = x0 - pre[i];
-    const int it = (int)(rem / nch), ch0 = (int)(rem - (long long)it * nch);
-    const int hk = it / nblk, blk = it - hk * nblk, row0 = blk * R;
-    const int ch1 = (int)(x1 - x0 < nch - ch0 ? ch0 + (x1 - x0) : nch);
-    const long long item0 = x0 - ch0;
-    const int first_worker = kv4_worker(T_all, W, item0), slot = worker - first_worker;
-    const unsigned item = (unsigned)(b * a.Hkv + hk) * (unsigned)a.blocks + (unsigned)blk;
-    if (ch0 == 0 && lane == 0) a.item_n[item] = kv4_worker(T_all, W, item0 + nch - 1) - first_worker + 1;
-    x0 += ch1 - ch0;
 
     // chunk ch holds keys k0 .. k1-1 (kv4_chunk, with what does not change taken out)
     const int* table = a.table + (size_t)b * a.g.max_pages;
@@ -414,8 +375,9 @@ __global__ void __launch_bounds__(kScoreThreads, R <= 8 ? 2 : 1) kv4_scores_kern
     };
     const char* lane_codes = reinterpret_cast<const char*>(a.k_codes) +
                              (((size_t)hk << a.g.page_shift) + key) * kTokenB + c * 4 * G;
-    const char* lane_meta = reinterpret_cast<const char*>(a.k_meta) + (((size_t)hk << a.g.page_shift) + key) * kMetaB;
-    uint32_t w[U][2][G], mt[U][2][G];
+    const char* lane_meta = reinterpret_cast<const char*>(a.k_meta) + (((size_t)hk << a.g.page_shift) + key) * kMetaB +
+                            (PAIR ? (c >> 1) * 4 * GS : 0);
+    uint32_t w[U][2][G], mt[U][2][GS];   // codes, and the pairs of the groups that the lane scales
     // a chunk's tiles into w and mt; a tile that is not there reads the pool's first page
     // instead, and no row sees it.  Returns which tiles are there.
     auto load_chunk = [&](int ch, int pages) {
@@ -429,7 +391,7 @@ __global__ void __launch_bounds__(kScoreThreads, R <= 8 ? 2 : 1) kv4_scores_kern
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 load_words<G>(reinterpret_cast<const uint32_t*>(pc + 8 * h * kTokenB), w[u][h]);
-                load_words<G>(reinterpret_cast<const uint32_t*>(pm + 8 * h * kMetaB), mt[u][h]);
+                load_words<GS>(reinterpret_cast<const uint32_t*>(pm + 8 * h * kMetaB), mt[u][h]);
             }
         }
         return __ballot_sync(kFull, pages >= 0);
@@ -438,13 +400,15 @@ __global__ void __launch_bounds__(kScoreThreads, R <= 8 ? 2 : 1) kv4_scores_kern
     int pages = page_of(ch0 + 1);
 
     // ---- queries: lane (n = lane / 4, c = lane % 4) holds dimensions 32 w + 8 c + i of row n
-    uint32_t qf[NT][G][4], ql[F32 ? NT : 1][G][4];   // B operands; float32 rows: high and low parts
+    // (PAIR: row n % 4, and of its two groups the one that columns 0-3 or 4-7 take)
+    constexpr int QG = PAIR ? GS : G;
+    uint32_t qf[NT][QG][4], ql[F32 ? NT : 1][QG][4];   // B operands; float32 rows: high and low parts
     uint32_t qz[NT][3];                              // sum q of group c in three parts
     float mul = 0.f, mul2 = 1.f;                     // of row lrow: x = mul mul2 acc
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-        const int r = row0 + nt * 8 + key;
-        const bool real = r < nrows && nt * 8 + key < R;
+        const int col = PAIR ? key & 3 : key, r = row0 + nt * 8 + col;
+        const bool real = r < nrows && nt * 8 + col < R;
         const int l = real ? r / a.group : 0, gi = real ? r - l * a.group : 0;
         const T* q = static_cast<const T*>(a.q) + (((size_t)b * a.Hkv * a.group + hk * a.group + gi) * a.g.L + l) * D;
         float x[G][8];
@@ -468,12 +432,22 @@ __global__ void __launch_bounds__(kScoreThreads, R <= 8 ? 2 : 1) kv4_scores_kern
         float zsum = 0.f;
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-            float sum = 0.f, y[8], lo[8];
+            float sum = 0.f;
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                y[k] = x[g][k] * fe;
-                sum += y[k];
+                x[g][k] *= fe;
+                sum += x[g][k];
             }
+            sum += __shfl_xor_sync(kFull, sum, 1);
+            sum += __shfl_xor_sync(kFull, sum, 2);
+            if (PAIR && G == 2 ? 2 * g == c : g == c) zsum = sum * 5.9604644775390625e-08f;   // 2^-24, the codes' unit
+        }
+        if (PAIR && key >= 4) zsum = 0.f;   // (the zero terms go to columns 0-3)
+#pragma unroll
+        for (int g = 0; g < QG; ++g) {
+            float y[8], lo[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) y[k] = PAIR && key >= 4 ? x[(g + GS) % G][k] : x[g][k];
             if constexpr (F32) {
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
@@ -493,9 +467,6 @@ __global__ void __launch_bounds__(kScoreThreads, R <= 8 ? 2 : 1) kv4_scores_kern
                 ql[nt][g][2] = pack_half(lo[2], lo[6]);
                 ql[nt][g][3] = pack_half(lo[3] * f, lo[7] * f);
             }
-            sum += __shfl_xor_sync(kFull, sum, 1);
-            sum += __shfl_xor_sync(kFull, sum, 2);
-            if (g == c) zsum = sum * 5.9604644775390625e-08f;   // 2^-24, the codes' unit
         }
         qz[nt][0] = bf16_part(zsum);
         qz[nt][1] = bf16_part(zsum);
@@ -517,8 +488,6 @@ __global__ void __launch_bounds__(kScoreThreads, R <= 8 ? 2 : 1) kv4_scores_kern
     const int pos_last = s.start + (kv4_min(row0 + R, nrows) - 1) / a.group;
     float m = -INFINITY;    // of the row, over the run so far (and what other warps told)
     int n = 0;              // candidates of the row so far
-    volatile unsigned long long* mine = &pub[warp][lrow];
-    if (sub == 0) *mine = (unsigned long long)item << 32 | 0xff800000u;
 
     // ---- keys, a chunk of U tiles at a time
 #pragma unroll 1
@@ -527,41 +496,69 @@ __global__ void __launch_bounds__(kScoreThreads, R <= 8 ? 2 : 1) kv4_scores_kern
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             float acc[NT][4];
-            uint32_t mz[2];   // the pair of group c (lanes past the groups: zeros)
+            uint32_t mz[2];   // the pair of group c (PAIR with two groups: of group c/2; else zeros)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                mz[h] = c == 0 ? mt[u][h][0] : 0u;
+                if constexpr (PAIR && G == 4) mz[h] = c & 1 ? mt[u][h][GS - 1] : mt[u][h][0];
+                else if constexpr (PAIR) mz[h] = c & 1 ? 0u : mt[u][h][0];
+                else {
+                    mz[h] = c == 0 ? mt[u][h][0] : 0u;
 #pragma unroll
-                for (int g = 1; g < G; ++g) mz[h] = c == g ? mt[u][h][g] : mz[h];
+                    for (int g = 1; g < G; ++g) mz[h] = c == g ? mt[u][h][g] : mz[h];
+                }
             }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 mma_16816_bf_0(acc[nt], mz[0], mz[1], mz[0], mz[1], qz[nt][0], qz[nt][1]);
                 mma_1688_bf(acc[nt], mz[0], mz[1], qz[nt][2]);
             }
+            // a word's codes as four pairs of halves
+            auto halves = [](uint32_t x, uint32_t (&h)[4]) {
+                h[0] = x & 0x000f000fu;
+                h[1] = x & 0x00f000f0u;
+                x >>= 8;
+                h[2] = x & 0x000f000fu;
+                h[3] = x & 0x00f000f0u;
+            };
 #pragma unroll
-            for (int g = 0; g < G; ++g) {
-                uint32_t w0 = w[u][0][g], w1 = w[u][1][g];
-                uint32_t av[8];
-                av[0] = w0 & 0x000f000fu; av[1] = w1 & 0x000f000fu;
-                av[2] = w0 & 0x00f000f0u; av[3] = w1 & 0x00f000f0u;
-                w0 >>= 8; w1 >>= 8;
-                av[4] = w0 & 0x000f000fu; av[5] = w1 & 0x000f000fu;
-                av[6] = w0 & 0x00f000f0u; av[7] = w1 & 0x00f000f0u;
+            for (int g = 0; g < GS; ++g) {
                 const float s0 = bf16_lo(mt[u][0][g]), s1 = bf16_lo(mt[u][1][g]);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
+                uint32_t k0h[4], k1h[4];
+                halves(w[u][0][g], k0h);
+                halves(w[u][1][g], k1h);
+                if constexpr (PAIR) {
+                    uint32_t o0[4], o1[4];   // the second group's
+                    halves(w[u][0][g + GS], o0);
+                    halves(w[u][1][g + GS], o1);
+                    const bool one = key < 4;
                     float d[4];
-                    mma_16816_0(d, av[0], av[1], av[2], av[3], qf[nt][g][0], qf[nt][g][1]);
-                    mma_16816(d, av[4], av[5], av[6], av[7], qf[nt][g][2], qf[nt][g][3]);
-                    if constexpr (F32) {
-                        mma_16816(d, av[0], av[1], av[2], av[3], ql[nt][g][0], ql[nt][g][1]);
-                        mma_16816(d, av[4], av[5], av[6], av[7], ql[nt][g][2], ql[nt][g][3]);
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+                        const uint32_t b0 = one ? qf[0][g][t] : 0u, b1 = one ? 0u : qf[0][g][t];
+                        if (t == 0) mma_16816_0(d, k0h[t], k1h[t], o0[t], o1[t], b0, b1);
+                        else mma_16816(d, k0h[t], k1h[t], o0[t], o1[t], b0, b1);
+                        if constexpr (F32)
+                            mma_16816(d, k0h[t], k1h[t], o0[t], o1[t], one ? ql[0][g][t] : 0u, one ? 0u : ql[0][g][t]);
                     }
-                    acc[nt][0] = fmaf(s0, d[0], acc[nt][0]);
-                    acc[nt][1] = fmaf(s0, d[1], acc[nt][1]);
-                    acc[nt][2] = fmaf(s1, d[2], acc[nt][2]);
-                    acc[nt][3] = fmaf(s1, d[3], acc[nt][3]);
+                    acc[0][0] = fmaf(s0, d[0], acc[0][0]);
+                    acc[0][1] = fmaf(s0, d[1], acc[0][1]);
+                    acc[0][2] = fmaf(s1, d[2], acc[0][2]);
+                    acc[0][3] = fmaf(s1, d[3], acc[0][3]);
+                } else {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        float d[4];
+                        mma_16816_0(d, k0h[0], k1h[0], k0h[1], k1h[1], qf[nt][g][0], qf[nt][g][1]);
+                        mma_16816(d, k0h[2], k1h[2], k0h[3], k1h[3], qf[nt][g][2], qf[nt][g][3]);
+                        if constexpr (F32) {
+                            mma_16816(d, k0h[0], k1h[0], k0h[1], k1h[1], ql[nt][g][0], ql[nt][g][1]);
+                            mma_16816(d, k0h[2], k1h[2], k0h[3], k1h[3], ql[nt][g][2], ql[nt][g][3]);
+                        }
+                        acc[nt][0] = fmaf(s0, d[0], acc[nt][0]);
+                        acc[nt][1] = fmaf(s0, d[1], acc[nt][1]);
+                        acc[nt][2] = fmaf(s1, d[2], acc[nt][2]);
+                        acc[nt][3] = fmaf(s1, d[3], acc[nt][3]);
+                    }
                 }
             }
 #pragma unroll
@@ -586,7 +583,11 @@ __global__ void __launch_bounds__(kScoreThreads, R <= 8 ? 2 : 1) kv4_scores_kern
         float v[KPL];
 #pragma unroll
         for (int k = 0; k < KPL / 4; ++k) {
-            const float4 f = *reinterpret_cast<const float4*>(xs + lrow * kStride + (k * LPR + sub) * 4);
+            float4 f = *reinterpret_cast<const float4*>(xs + lrow * kStride + (k * LPR + sub) * 4);
+            if constexpr (PAIR) {   // the second groups' share
+                const float4 h = *reinterpret_cast<const float4*>(xs + (lrow + 4) * kStride + (k * LPR + sub) * 4);
+                f = make_float4(f.x + h.x, f.y + h.y, f.z + h.z, f.w + h.w);
+            }
             v[4 * k] = f.x * mul; v[4 * k + 1] = f.y * mul; v[4 * k + 2] = f.z * mul; v[4 * k + 3] = f.w * mul;
         }
         if (mul2 != 1.f) {
@@ -601,16 +602,14 @@ __global__ void __launch_bounds__(kScoreThreads, R <= 8 ? 2 : 1) kv4_scores_kern
                 v[k] = see ? v[k] : -INFINITY;
             }
         }
-        // a NaN passes through every maximum; +inf is caught at the end
-        for (int o = sub; o < kScoreWarps; o += LPR) {
-            const unsigned long long p = *const_cast<volatile unsigned long long*>(&pub[o][lrow]);
-            if ((unsigned)(p >> 32) == item) m = max_nan(m, __uint_as_float((unsigned)p));
-        }
+        // a NaN passes through every maximum; +inf is caught at the end.  (A store of row_max that
+        // loses to another warp's costs a weaker filter, no more.)
+        m = max_nan(m, *const_cast<volatile float*>(&row_max[lrow]));
 #pragma unroll
         for (int k = 0; k < KPL; ++k) m = max_nan(m, v[k]);
 #pragma unroll
         for (int o = 1; o < LPR; o <<= 1) m = max_nan(m, __shfl_xor_sync(kFull, m, o));
-        if (sub == 0) *mine = (unsigned long long)item << 32 | __float_as_uint(m);
+        if (sub == 0) *const_cast<volatile float*>(&row_max[lrow]) = m;
         // above m - 1, and the maximum itself: where |m| >= 2^24 makes them equal, the limit is
         // the next float below m (m = -inf or NaN: it is NaN, and nothing is above)
         float lim = m - 1.f;
@@ -634,18 +633,17 @@ __global__ void __launch_bounds__(kScoreThreads, R <= 8 ? 2 : 1) kv4_scores_kern
             const int k = __ffs(take) - 1;
             take &= take - 1u;
             const int kk = ((k >> 2) * LPR + sub) * 4 + (k & 3);
-            out[put++] = make_int2(__float_as_int(xs[lrow * kStride + kk] * mul * mul2), k0 + kk);
+            float x = xs[lrow * kStride + kk];
+            if constexpr (PAIR) x += xs[(lrow + 4) * kStride + kk];
+            out[put++] = make_int2(__float_as_int(x * mul * mul2), k0 + kk);
         }
         __syncwarp();
     }
-    if (lreal && sub == 0) {
-        a.run_max[grow * a.nslot + slot] = m < INFINITY ? m : nanf("");
-        a.run_n[grow * a.nslot + slot] = n;
-        a.run_at[grow * a.nslot + slot] = ch0;
-    }
-    __syncwarp();
-    }   // items of this warp's share
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (lreal && sub == 0) {
+        a.run_max[grow * a.nrun + slot] = m < INFINITY ? m : nanf("");
+        a.run_n[grow * a.nrun + slot] = n;
+    }
 }
 
 // ------------------------------------------------------------------ solve and P.V
@@ -689,8 +687,7 @@ __global__ void __launch_bounds__(kSolveThreads) kv4_solve_kernel(const Kv4Args 
     extern __shared__ int solve_smem[];
     float* ys = reinterpret_cast<float*>(solve_smem);   // [kCap] x - m of the candidates, then their weights
     int* js = solve_smem + kCap;                        // [kCap] their keys
-    int* lst = js + kCap;               // [nslot] where the runs' lists begin in the row's part of the workspace
-    int* off = lst + a.nslot;           // [nslot + 1] the runs' candidates before each run
+    int* off = js + kCap;               // [nrun + 1] the runs' candidates before each run
     __shared__ float red[3][kSolveWarps];
     __shared__ int box[kSolveWarps], box2[kSolveWarps];
     __shared__ float bc[2];
@@ -703,15 +700,18 @@ __global__ void __launch_bounds__(kSolveThreads) kv4_solve_kernel(const Kv4Args 
     const Kv4Seq s = seq_of(a, b);
     const size_t orow = ((size_t)b * a.Hkv * a.group + hk * a.group + gi) * a.g.L + l;
     T* o = static_cast<T*>(a.o) + orow * D;
-    const size_t at = ((size_t)bk * per + r) * a.nslot;
+    const size_t at = ((size_t)bk * per + r) * a.nrun;
     const float* cm = a.run_max + at;
     int* cn = a.run_n + at;
-    const int* cat = a.run_at + at;
     int2* cand = a.cand + ((size_t)bk * per + r) * a.nchunk * a.chunk;
-    auto list_of = [&](int i) { return cand + lst[i]; };
+    int nrun = 0, stride = 0;   // the sequence's runs, entries from one's list to the next's
+    if (l < s.rows) {
+        const int nch = kv4_seq_chunks(a.g, s, a.chunk), run = kv4_run(nch, a.nrun);
+        stride = run * a.chunk;   // (a row's part holds at most 2^30 entries)
+        nrun = (nch + run - 1) / run;
+    }
+    auto list_of = [&](int i) { return cand + (size_t)i * stride; };
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const bool seen = l < s.rows && kv4_seq_chunks(a.g, s, a.chunk) > 0;
-    const int nrun = seen ? a.item_n[(size_t)bk * a.blocks + r / a.block] : 0;
 
     // ---- row maximum (every warp for itself), then the runs' offsets, a quarter each warp
     float m = -INFINITY;
@@ -742,10 +742,7 @@ __global__ void __launch_bounds__(kSolveThreads) kv4_solve_kernel(const Kv4Args 
             const int y = __shfl_up_sync(kFull, incl, d);
             if (lane >= d) incl += y;
         }
-        if (i < c1) {
-            off[i] = sum + incl - n;
-            lst[i] = cat[i] * a.chunk;   // (a row's part holds at most 2^30 entries)
-        }
+        if (i < c1) off[i] = sum + incl - n;
         sum += __shfl_sync(kFull, incl, 31);
     }
     int raw;
@@ -763,7 +760,7 @@ __global__ void __launch_bounds__(kSolveThreads) kv4_solve_kernel(const Kv4Args 
     auto each = [&](auto f) {
         int i = 0;   // the run that holds entry part0 (by halving), then forward
 #pragma unroll 1
-        for (int step = 2048; step > 0; step >>= 1)
+        for (int step = kKvMaxRuns / 2; step > 0; step >>= 1)
             if (i + step < nrun && off[i + step] <= part0) i += step;
         constexpr int U = 4;
 #pragma unroll 1
@@ -1013,7 +1010,8 @@ cudaError_t write_or_read(const Kv4Args& a, bool write, cudaStream_t s) {
 
 template <typename T, int D, int R>
 cudaError_t launch_scores(const Kv4Args& a, cudaStream_t s) {
-    kv4_scores_kernel<T, D, R><<<dim3(a.ctas, (a.g.B + a.seqs - 1) / a.seqs), kScoreThreads, 0, s>>>(a);
+    const dim3 grid((a.nrun + kScoreWarps - 1) / kScoreWarps, a.blocks, a.g.B * a.Hkv);
+    kv4_scores_kernel<T, D, R><<<grid, kScoreThreads, 0, s>>>(a);
     return cudaGetLastError();
 }
 
@@ -1030,7 +1028,7 @@ cudaError_t attn(const Kv4Args& a, int gm, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.g.B * a.Hkv * a.g.L * a.group));
     cfg.blockDim = dim3(kSolveThreads);
-    cfg.dynamicSmemBytes = (size_t)(2 * kCap + 2 * a.nslot + 1) * 4;
+    cfg.dynamicSmemBytes = (size_t)(2 * kCap + a.nrun + 1) * 4;
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -118,16 +118,9 @@ ENT_HD void kv4_chunk(const Kv4Geom& g, const Kv4Seq& s, int C, int c, int* k0, 
     }
 }
 
-// The T chunks of a group of sequences (every key head and block of rows of each, one after
-// the other) are dealt to W workers in equal contiguous shares: worker w takes chunks
-// kv4_share(T, W, w) .. kv4_share(T, W, w + 1) - 1, and chunk y belongs to kv4_worker(T, W, y).
-// No more workers than half the chunks, so that none is without one.
-ENT_HD int kv4_workers(long long T, int most) {
-    const long long w = (T + 1) / 2;
-    return w < most ? (int)w : most;
-}
-ENT_HD long long kv4_share(long long T, int W, int w) { return (long long)w * T / W; }
-ENT_HD int kv4_worker(long long T, int W, long long y) { return (int)(((y + 1) * W - 1) / T); }
+// The chunks of a sequence are dealt to `nrun` runs of equal length: run i holds chunks
+// [i * kv4_run, (i + 1) * kv4_run) below kv4_seq_chunks.
+ENT_HD int kv4_run(int seq_chunks, int nrun) { return (seq_chunks + nrun - 1) / nrun; }
 
 // Whether the row at position pos sees key j.
 ENT_HD bool kv4_sees(const Kv4Geom& g, int pos, int j) {

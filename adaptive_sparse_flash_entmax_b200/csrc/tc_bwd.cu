@@ -324,11 +324,6 @@ tc_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const float tau = row_valid ? a.tau[(size_t)bh * N + i] : 0.f;
         float* xch = reinterpret_cast<float*>(smem + L::kXch);   // [5][2][128]
         const float2 cx2 = make_float2(cx, cx), nt2 = make_float2(-tau, -tau);
-        // window: column c of the columns from key key0 on is seen iff c >= lo or c < sk,
-        // lo = wlo - key0, sk = sinks - key0
-        const int wlo = i - a.window + 1;
-        auto seen = [&](int key0, int c) { return c >= wlo - key0 || c < a.sinks - key0; };
-        auto seen_all = [&](int key0) { return wlo - key0 <= 0 || wlo <= a.sinks || a.sinks - key0 >= 64; };
         bool ok = true;
         // phase A: sum_j g and sum_j g dP
         float sg = 0.f, sgdp = 0.f;
@@ -350,9 +345,15 @@ tc_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             if (lane == 0) mbar_arrive(&s_empty[p]);
             const int key0 = list[j] * kBlk + half * 64;
             const int nv = key_end - key0;
-            if (!__all_sync(0xffffffffu, nv >= 64 && (!WIN || seen_all(key0)))) {   // diagonal, ragged or window edge
+            if constexpr (WIN) {
+                const unsigned long long see = win_cols64(a.window, a.sinks, i, key0, nv);
+                if (!__all_sync(0xffffffffu, see == ~0ull)) {
 #pragma unroll
-                for (int c = 0; c < 64; ++c) sa[c] = (c < nv && (!WIN || seen(key0, c))) ? sa[c] : -INFINITY;
+                    for (int c = 0; c < 64; ++c) sa[c] = (see >> c & 1ull) ? sa[c] : -INFINITY;
+                }
+            } else if (!__all_sync(0xffffffffu, nv >= 64)) {   // diagonal or ragged block
+#pragma unroll
+                for (int c = 0; c < 64; ++c) sa[c] = (c < nv) ? sa[c] : -INFINITY;
             }
             float2 a0 = make_float2(0.f, 0.f), b0 = a0, a1 = a0, b1 = a0;
 #pragma unroll
@@ -432,9 +433,15 @@ tc_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s_empty[p]);
                 const int nv = key_end - key0;   // valid columns of this thread: c < nv
-                if (!__all_sync(0xffffffffu, nv >= 64 && (!WIN || seen_all(key0)))) {   // diagonal, ragged or window edge
+                if constexpr (WIN) {
+                    const unsigned long long see = win_cols64(a.window, a.sinks, i, key0, nv);
+                    if (!__all_sync(0xffffffffu, see == ~0ull)) {
 #pragma unroll
-                    for (int c = 0; c < 64; ++c) sa[c] = (c < nv && (!WIN || seen(key0, c))) ? sa[c] : -INFINITY;
+                        for (int c = 0; c < 64; ++c) sa[c] = (see >> c & 1ull) ? sa[c] : -INFINITY;
+                    }
+                } else if (!__all_sync(0xffffffffu, nv >= 64)) {   // diagonal or ragged block
+#pragma unroll
+                    for (int c = 0; c < 64; ++c) sa[c] = (c < nv) ? sa[c] : -INFINITY;
                 }
             }
             uint32_t whi[32];

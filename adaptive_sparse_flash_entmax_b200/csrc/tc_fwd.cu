@@ -143,16 +143,6 @@ struct SpecJob {
     }
 };
 
-// Window columns of query i in the columns from key `key0` on: column c is seen iff
-// c >= lo or c < sk (and c is not past the query).
-struct WinCols {
-    int lo, sk;
-    __device__ __forceinline__ WinCols(const FwdArgs& a, int i, int key0)
-        : lo(i - a.window + 1 - key0), sk(a.sinks - key0) {}
-    __device__ __forceinline__ bool sees(int c) const { return c >= lo || c < sk; }
-    __device__ __forceinline__ bool all(int n) const { return lo <= 0 || lo <= sk || sk >= n; }
-};
-
 // Bounded wait that ignores the abort flag (used to drain in-flight copies).
 __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
     const uint64_t t0 = globaltimer_ns();
@@ -697,12 +687,18 @@ tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                         if (lane == 0) mbar_arrive(&s_empty2[sb]);
                     }
                     const int nv = key_end - b * kBlk - c0;   // valid columns of this thread: c < nv
-                    const WinCols wc(a, i, b * kBlk + c0);
-                    const bool full_blk = __all_sync(0xffffffffu, nv >= 64 && (!WIN || wc.all(64)));
-                    if (!full_blk) {
+                    if constexpr (WIN) {
+                        const unsigned long long see = win_cols64(a.window, a.sinks, i, b * kBlk + c0, nv);
+                        if (!__all_sync(0xffffffffu, see == ~0ull)) {
 #pragma unroll
-                        for (int c = 0; c < 64; ++c)
-                            s[c] = (c < nv && (!WIN || wc.sees(c))) ? s[c] : -INFINITY;
+                            for (int c = 0; c < 64; ++c) s[c] = (see >> c & 1ull) ? s[c] : -INFINITY;
+                        }
+                    } else {
+                        const bool full_blk = __all_sync(0xffffffffu, nv >= 64);
+                        if (!full_blk) {
+#pragma unroll
+                            for (int c = 0; c < 64; ++c) s[c] = (c < nv) ? s[c] : -INFINITY;
+                        }
                     }
                     if (pass == 0) {
                         float m0 = s[0], m1 = s[1], m2 = s[2], m3 = s[3];
@@ -908,8 +904,9 @@ tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                 if (!(ok = mbar_wait(&s_full[sb], (li / SB) & 1, ab, 9))) break;
                 tc_fence_after();
                 const int nv = key_end - b * kBlk - c0;   // valid columns of this thread: c < nv
-                const WinCols wc(a, i, b * kBlk + c0);
-                const bool full_blk = __all_sync(0xffffffffu, nv >= 64 && (!WIN || wc.all(64)));
+                [[maybe_unused]] unsigned long long see = ~0ull;
+                if constexpr (WIN) see = win_cols64(a.window, a.sinks, i, b * kBlk + c0, nv);
+                const bool full_blk = __all_sync(0xffffffffu, WIN ? see == ~0ull : nv >= 64);
                 const float2 cx2 = make_float2(cx, cx), nt2 = make_float2(-sv.tau, -sv.tau);
                 uint32_t nzb = 0u;   // OR of this thread's bf16 p bits: nonzero iff some p > 0
                 // two rounds of 32 keys, each loaded, turned into P (and G) and stored over its
@@ -924,7 +921,8 @@ tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                     if (!full_blk) {
 #pragma unroll
                         for (int c = 0; c < 32; ++c)
-                            s[c] = (32 * hc + c < nv && (!WIN || wc.sees(32 * hc + c))) ? s[c] : -INFINITY;
+                            s[c] = (WIN ? (see >> c & 1ull) != 0ull : 32 * hc + c < nv) ? s[c] : -INFINITY;
+                        if constexpr (WIN) see >>= 32;   // (the next round's columns)
                     }
                     uint32_t pk[16];
                     [[maybe_unused]] uint32_t gk[16];

@@ -18,7 +18,7 @@ from typing import NamedTuple
 import torch
 
 from . import capi
-from .attention import _DTYPES, _raise, _stream_handle
+from .attention import _DTYPES, _on, _raise, _stream_handle
 
 _GROUP = 32
 
@@ -96,11 +96,8 @@ def _check_rows4(*ts):
 
 def _call(fn, device, *args):
     """fn(*args, stream) with the tensors' device current."""
-    if device.index == torch._C._cuda_getDevice():
+    with _on(device):
         st = fn(*args, _stream_handle(device))
-    else:
-        with torch.cuda.device(device):
-            st = fn(*args, _stream_handle(device))
     _raise(st, fn.__name__)
 
 

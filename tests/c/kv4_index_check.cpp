@@ -77,26 +77,12 @@ int main() {
             Kv4Geom far{1, 1, 2000000000, 20, 1, 1 << 20, 0, 0};
             CHECK(kv4_row(far, 8, 1999999999, 7, 5) == ((1999999999ull * 8 + 7) << 20) + 5);
         }
-    // shares of workers: every chunk belongs to one, none is empty, and the inverse agrees
-    for (long long T : {1ll, 2ll, 3ll, 7ll, 64ll, 1000ll, 2367ll, 2368ll, 2369ll, 100003ll})
-        for (int most : {1, 8, 16, 1184, 2368}) {
-            const int W = kv4_workers(T, most);
-            CHECK(W >= 1 && W <= most && W <= T);
-            CHECK(kv4_share(T, W, 0) == 0 && kv4_share(T, W, W) == T);
-            for (int w = 0; w < W; ++w) {
-                const long long x0 = kv4_share(T, W, w), x1 = kv4_share(T, W, w + 1);
-                CHECK(x0 < x1);
-                CHECK(kv4_worker(T, W, x0) == w && kv4_worker(T, W, x1 - 1) == w);
-            }
+    // runs: every chunk in one, and no more runs than there are places
+    for (int n : {1, 2, 3, 7, 64, 1000, 16384})
+        for (int nrun : {1, 2, 3, 37, 1024}) {
+            const int run = kv4_run(n, nrun);
+            CHECK(run >= 1 && (long long)run * nrun >= n && (n + run - 1) / run <= nrun);
         }
-    // (shares of the largest sums)
-    for (long long T : {1ll << 40, (1ll << 50) + 12345}) {
-        const int W = kv4_workers(T, 2368);
-        for (int w : {0, 1, 1000, 2367}) {
-            const long long x0 = kv4_share(T, W, w), x1 = kv4_share(T, W, w + 1);
-            CHECK(x0 >= 0 && x0 < x1 && kv4_worker(T, W, x0) == w && kv4_worker(T, W, x1 - 1) == w);
-        }
-    }
     // the largest cover
     for (int window : {0, 1, 1 << 30, 2147483647}) {
         Kv4Geom g{1, 3, 1, 4, 1 << 26, 1 << 30, window, window ? 2147483647 : 0};
