@@ -11,6 +11,7 @@
 // its chunk's maximum - 1 has p = 0: the scores never leave the chip but for the few that
 // can weigh, and value rows without a weight are never read.
 #include "kernels.h"
+#include "tc_common.cuh"
 
 #include <cuda_fp16.h>
 
@@ -262,7 +263,8 @@ __global__ void __launch_bounds__(kKvThreads) kv4_read_kernel(const Kv4Args a) {
 // in afterwards:
 //     q.k = sum_groups scale * (codes . q) + zero * sum q,
 // the second sum as a product too: a lane's pair of group c is two elements of an A operand,
-// met by (0, sum q of group c) in three bf16 parts (24 bits).
+// met by (0, sum q of group c) in three bf16 parts (24 bits); float32 rows take codes less 8
+// and (8 sum q, sum q).
 // The queries are fp16, scaled per row by a power of two so that the largest lies in
 // [2^14, 2^15): exact for bf16 values down to 2^-31 of the largest, below which the
 // rounding is 2^-39 of it; a float32 row is the sum of two such halves (22 bits).
@@ -305,31 +307,60 @@ __device__ __forceinline__ uint32_t bf16_part(float& x) {
     return (uint32_t)__bfloat16_as_ushort(h) << 16;
 }
 
-// G consecutive 4-byte words (one load)
+// G consecutive 4-byte words of shared memory (one load)
 template <int G>
-__device__ __forceinline__ void load_words(const uint32_t* p, uint32_t (&w)[G]) {
+__device__ __forceinline__ void load_words(const char* p, uint32_t (&w)[G]) {
     if constexpr (G == 4) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+        const uint4 v = *reinterpret_cast<const uint4*>(p);
         w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
     } else if constexpr (G == 2) {
-        const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+        const uint2 v = *reinterpret_cast<const uint2*>(p);
         w[0] = v.x; w[1] = v.y;
     } else {
-        w[0] = __ldg(p);
+        w[0] = *reinterpret_cast<const uint32_t*>(p);
     }
+}
+
+// `bytes` (a multiple of 16, as both addresses) from this GPU's memory into shared memory,
+// counted at `bar`
+__device__ __forceinline__ void bulk_copy(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     tc::smem_u32(dst)),
+                 "l"(src), "r"(bytes), "r"(tc::smem_u32(bar))
+                 : "memory");
+}
+
+// Waits for a phase, 2 s at most.
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity) {
+    if (tc::mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = tc::globaltimer_ns();
+    while (!tc::mbar_try_wait(bar, parity))
+        if (tc::globaltimer_ns() - t0 > tc::kWaitLimitNs) return false;
+    return true;
 }
 
 constexpr int kScoreWarps = 4;
 constexpr int kScoreThreads = kScoreWarps * 32;
+constexpr int kStages = 2;   // chunks of a warp in shared memory: one on its way while one is worked on
+
+template <int D, int R>
+struct ScoreSmem {   // of one warp
+    static constexpr int C = kv4_chunk_keys(R), kCodes = C * (D / 2), kMeta = C * (D / kKvGroup) * 4;
+    static constexpr int kStage = kCodes + kMeta;
+    static constexpr int kStride = C + 4;   // floats a row of scores: spreads a product's 8 keys x 4 row pairs over the banks
+    static constexpr int kBytes = kStages * kStage + (R <= 8 ? 8 : R) * kStride * 4;
+};
 
 // R: rows of a block (4, 8, 16 or 32), in NT products of 8 columns.
 template <typename T, int D, int R>
-__global__ void __launch_bounds__(kScoreThreads, R == 4 ? 5 : R == 8 ? 4 : 2) kv4_scores_kernel(const Kv4Args a) {
+__global__ void __launch_bounds__(kScoreThreads, R == 4 ? 4 : R == 8 ? 3 : 2) kv4_scores_kernel(const Kv4Args a) {
     constexpr int G = D / kKvGroup, NT = R <= 8 ? 1 : R / 8, C = kv4_chunk_keys(R), U = C / kKvTile;
     constexpr int LPR = 32 / R, KPL = C / LPR;   // lanes a row, keys a lane
-    constexpr int kStride = C + 4;   // spreads a product's 8 keys x 4 row pairs over the banks
+    using L = ScoreSmem<D, R>;
+    constexpr int kStride = L::kStride;
     constexpr bool F32 = sizeof(T) == 4;
-    __shared__ __align__(16) float xs_all[kScoreWarps][8 * NT * kStride];
+    extern __shared__ __align__(128) char score_smem[];
+    __shared__ uint64_t bars_all[kScoreWarps][kStages];
     // With four rows the product's 8 columns hold two groups of dimensions, h and h + G/2, each
     // MMA half of its contraction over either: columns 0-3 are the rows with the first group,
     // 4-7 with the second.  As many products, but half the scale multiplications.
@@ -337,7 +368,9 @@ __global__ void __launch_bounds__(kScoreThreads, R == 4 ? 5 : R == 8 ? 4 : 2) kv
     constexpr int GS = PAIR ? G / 2 : G;         // groups that a lane scales
     __shared__ float row_max[R];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    float* xs = xs_all[warp];
+    char* ring = score_smem + warp * L::kBytes;                       // [kStages][codes, meta]
+    float* xs = reinterpret_cast<float*>(ring + kStages * L::kStage);
+    uint64_t* bars = bars_all[warp];
     const int bk = blockIdx.z, b = bk / a.Hkv, hk = bk - b * a.Hkv;
     const Kv4Seq s = seq_of(a, b);
     if (s.bad && a.bad && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(a.bad, s.bad);
@@ -352,8 +385,13 @@ __global__ void __launch_bounds__(kScoreThreads, R == 4 ? 5 : R == 8 ? 4 : 2) kv
     const int c = lane & 3, key = lane >> 2;   // the lane's keys of a tile: key and key + 8
     const int lrow = lane / LPR, sub = lane % LPR;   // the row that it looks through, and its part of it
     constexpr int kTokenB = D / 2, kMetaB = 4 * G;   // bytes of a token
-    const size_t page_rows = (size_t)a.Hkv << a.g.page_shift;
-    const int mask = (1 << a.g.page_shift) - 1;
+    if (lane == 0) {
+#pragma unroll
+        for (int i = 0; i < kStages; ++i) tc::mbar_init(&bars[i], 1);
+        tc::fence_barrier_init();
+        tc::fence_proxy_async_smem();
+    }
+    __syncwarp();
 
     // chunk ch holds keys k0 .. k1-1 (kv4_chunk, with what does not change taken out)
     const int* table = a.table + (size_t)b * a.g.max_pages;
@@ -373,37 +411,35 @@ __global__ void __launch_bounds__(kScoreThreads, R == 4 ? 5 : R == 8 ? 4 : 2) kv
         }
         return p;
     };
-    const char* lane_codes = reinterpret_cast<const char*>(a.k_codes) +
-                             (((size_t)hk << a.g.page_shift) + key) * kTokenB + c * 4 * G;
-    const char* lane_meta = reinterpret_cast<const char*>(a.k_meta) + (((size_t)hk << a.g.page_shift) + key) * kMetaB +
-                            (PAIR ? (c >> 1) * 4 * GS : 0);
-    uint32_t w[U][2][G], mt[U][2][GS];   // codes, and the pairs of the groups that the lane scales
-    // a chunk's tiles into w and mt; a tile that is not there reads the pool's first page
-    // instead, and no row sees it.  Returns which tiles are there.
-    auto load_chunk = [&](int ch, int pages) {
-        const int k0 = first_key(ch);
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int page = max(__shfl_sync(kFull, pages, u), 0);
-            const size_t row = page * page_rows + ((k0 + u * kKvTile) & mask);
-            const char* pc = lane_codes + row * kTokenB;
-            const char* pm = lane_meta + row * kMetaB;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                load_words<G>(reinterpret_cast<const uint32_t*>(pc + 8 * h * kTokenB), w[u][h]);
-                load_words<GS>(reinterpret_cast<const uint32_t*>(pm + 8 * h * kMetaB), mt[u][h]);
-            }
+    // Starts the copies of a chunk into its stage, a tile a lane; what is not there is not
+    // copied, and no row sees it.  `has`: four bits a stage, the tiles that are there.
+    unsigned has = 0;
+    int next_stage = 0, pages = page_of(ch0);
+    auto issue = [&](int ch) {
+        const unsigned there = __ballot_sync(kFull, pages >= 0);
+        uint64_t* bar = &bars[next_stage];
+        if (lane == 0) tc::mbar_arrive_expect_tx(bar, __popc(there) * (kKvTile * (kTokenB + kMetaB)));
+        __syncwarp();
+        if (pages >= 0) {
+            char* dst = ring + next_stage * L::kStage;
+            const size_t row = kv4_row(a.g, a.Hkv, pages, hk, first_key(ch) + lane * kKvTile);
+            bulk_copy(dst + lane * kKvTile * kTokenB, reinterpret_cast<const char*>(a.k_codes) + row * kTokenB,
+                      kKvTile * kTokenB, bar);
+            bulk_copy(dst + L::kCodes + lane * kKvTile * kMetaB, reinterpret_cast<const char*>(a.k_meta) + row * kMetaB,
+                      kKvTile * kMetaB, bar);
         }
-        return __ballot_sync(kFull, pages >= 0);
+        has = (has & ~(15u << (4 * next_stage))) | there << (4 * next_stage);
+        next_stage = next_stage + 1 == kStages ? 0 : next_stage + 1;
+        pages = page_of(ch + 1);
     };
-    unsigned has = load_chunk(ch0, page_of(ch0));
-    int pages = page_of(ch0 + 1);
+    for (int i = 0; i < kStages - 1 && ch0 + i < ch1; ++i) issue(ch0 + i);
 
     // ---- queries: lane (n = lane / 4, c = lane % 4) holds dimensions 32 w + 8 c + i of row n
     // (PAIR: row n % 4, and of its two groups the one that columns 0-3 or 4-7 take)
     constexpr int QG = PAIR ? GS : G;
     uint32_t qf[NT][QG][4], ql[F32 ? NT : 1][QG][4];   // B operands; float32 rows: high and low parts
     uint32_t qz[NT][3];                              // sum q of group c in three parts
+    uint32_t qb[PAIR ? QG : 1][4][2], qbl[PAIR && F32 ? QG : 1][4][2];   // PAIR: the two halves of the operand
     float mul = 0.f, mul2 = 1.f;                     // of row lrow: x = mul mul2 acc
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -468,9 +504,15 @@ __global__ void __launch_bounds__(kScoreThreads, R == 4 ? 5 : R == 8 ? 4 : 2) kv
                 ql[nt][g][3] = pack_half(lo[3] * f, lo[7] * f);
             }
         }
-        qz[nt][0] = bf16_part(zsum);
-        qz[nt][1] = bf16_part(zsum);
-        qz[nt][2] = bf16_part(zsum);
+#pragma unroll
+        for (int t = 0; t < 3; ++t) {
+            qz[nt][t] = bf16_part(zsum);
+            // float32: the codes are less 8, and the pair's scale meets 8 times the sum
+            if constexpr (F32) {
+                const float part = __uint_as_float(qz[nt][t]) * 8.f;
+                qz[nt][t] |= __float_as_uint(part) >> 16;
+            }
+        }
         // x = cx 2^(24 - e) s, in two factors where one would overflow (24 - e <= 137);
         // a row with a NaN or an infinity has NaN scores
         const int e1 = min(24 - e, 100);
@@ -478,6 +520,19 @@ __global__ void __launch_bounds__(kScoreThreads, R == 4 ? 5 : R == 8 ? 4 : 2) kv
         const float f2 = __int_as_float((24 - e - e1 + 127) << 23);
         const float g1 = __shfl_sync(kFull, f1, 4 * (lrow & 7)), g2 = __shfl_sync(kFull, f2, 4 * (lrow & 7));
         if (lrow >> 3 == nt) { mul = g1; mul2 = g2; }
+    }
+    if constexpr (PAIR) {
+#pragma unroll
+        for (int g = 0; g < QG; ++g)
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                qb[g][t][0] = key < 4 ? qf[0][g][t] : 0u;
+                qb[g][t][1] = key < 4 ? 0u : qf[0][g][t];
+                if constexpr (F32) {
+                    qbl[g][t][0] = key < 4 ? ql[0][g][t] : 0u;
+                    qbl[g][t][1] = key < 4 ? 0u : ql[0][g][t];
+                }
+            }
     }
 
     const bool lreal = row0 + lrow < nrows;
@@ -490,21 +545,36 @@ __global__ void __launch_bounds__(kScoreThreads, R == 4 ? 5 : R == 8 ? 4 : 2) kv
     int n = 0;              // candidates of the row so far
 
     // ---- keys, a chunk of U tiles at a time
+    const char* lane_codes = ring + key * kTokenB + c * 4 * G;
+    const char* lane_meta = ring + L::kCodes + key * kMetaB + (PAIR ? (c >> 1) * 4 * GS : 0);
+    int stage = 0, phase = 0;
+    bool ok = true;
 #pragma unroll 1
     for (int ch = ch0; ch < ch1; ++ch) {
+        // (the stage of the chunk before this one, which every lane has read)
+        if (ch + kStages - 1 < ch1) issue(ch + kStages - 1);
         const int k0 = first_key(ch), k1 = end_key(ch, k0);
+        const unsigned there = has >> (4 * stage) & 15u;
+        ok = wait_phase(&bars[stage], phase);
+        if (!__all_sync(kFull, ok)) { ok = false; break; }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
+            uint32_t w[2][G], mt[2][GS];   // codes, and the pairs of the groups that the lane scales
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                load_words<G>(lane_codes + stage * L::kStage + (u * kKvTile + 8 * h) * kTokenB, w[h]);
+                load_words<GS>(lane_meta + stage * L::kStage + (u * kKvTile + 8 * h) * kMetaB, mt[h]);
+            }
             float acc[NT][4];
             uint32_t mz[2];   // the pair of group c (PAIR with two groups: of group c/2; else zeros)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                if constexpr (PAIR && G == 4) mz[h] = c & 1 ? mt[u][h][GS - 1] : mt[u][h][0];
-                else if constexpr (PAIR) mz[h] = c & 1 ? 0u : mt[u][h][0];
+                if constexpr (PAIR && G == 4) mz[h] = c & 1 ? mt[h][GS - 1] : mt[h][0];
+                else if constexpr (PAIR) mz[h] = c & 1 ? 0u : mt[h][0];
                 else {
-                    mz[h] = c == 0 ? mt[u][h][0] : 0u;
+                    mz[h] = c == 0 ? mt[h][0] : 0u;
 #pragma unroll
-                    for (int g = 1; g < G; ++g) mz[h] = c == g ? mt[u][h][g] : mz[h];
+                    for (int g = 1; g < G; ++g) mz[h] = c == g ? mt[h][g] : mz[h];
                 }
             }
 #pragma unroll
@@ -512,33 +582,40 @@ __global__ void __launch_bounds__(kScoreThreads, R == 4 ? 5 : R == 8 ? 4 : 2) kv
                 mma_16816_bf_0(acc[nt], mz[0], mz[1], mz[0], mz[1], qz[nt][0], qz[nt][1]);
                 mma_1688_bf(acc[nt], mz[0], mz[1], qz[nt][2]);
             }
-            // a word's codes as four pairs of halves
+            // a word's codes as four pairs of halves; for float32 queries less 8, which takes the
+            // cancellation between the codes' term and the zeros' out of the float sums
             auto halves = [](uint32_t x, uint32_t (&h)[4]) {
                 h[0] = x & 0x000f000fu;
                 h[1] = x & 0x00f000f0u;
                 x >>= 8;
                 h[2] = x & 0x000f000fu;
                 h[3] = x & 0x00f000f0u;
+                if constexpr (F32) {
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+                        const uint32_t eight = t & 1 ? 0x00800080u : 0x00080008u;   // 8 of the same unit
+                        const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&h[t]),
+                                                  *reinterpret_cast<const __half2*>(&eight));
+                        h[t] = *reinterpret_cast<const uint32_t*>(&y);
+                    }
+                }
             };
 #pragma unroll
             for (int g = 0; g < GS; ++g) {
-                const float s0 = bf16_lo(mt[u][0][g]), s1 = bf16_lo(mt[u][1][g]);
+                const float s0 = bf16_lo(mt[0][g]), s1 = bf16_lo(mt[1][g]);
                 uint32_t k0h[4], k1h[4];
-                halves(w[u][0][g], k0h);
-                halves(w[u][1][g], k1h);
+                halves(w[0][g], k0h);
+                halves(w[1][g], k1h);
                 if constexpr (PAIR) {
                     uint32_t o0[4], o1[4];   // the second group's
-                    halves(w[u][0][g + GS], o0);
-                    halves(w[u][1][g + GS], o1);
-                    const bool one = key < 4;
+                    halves(w[0][g + GS], o0);
+                    halves(w[1][g + GS], o1);
                     float d[4];
 #pragma unroll
                     for (int t = 0; t < 4; ++t) {
-                        const uint32_t b0 = one ? qf[0][g][t] : 0u, b1 = one ? 0u : qf[0][g][t];
-                        if (t == 0) mma_16816_0(d, k0h[t], k1h[t], o0[t], o1[t], b0, b1);
-                        else mma_16816(d, k0h[t], k1h[t], o0[t], o1[t], b0, b1);
-                        if constexpr (F32)
-                            mma_16816(d, k0h[t], k1h[t], o0[t], o1[t], one ? ql[0][g][t] : 0u, one ? 0u : ql[0][g][t]);
+                        if (t == 0) mma_16816_0(d, k0h[t], k1h[t], o0[t], o1[t], qb[g][t][0], qb[g][t][1]);
+                        else mma_16816(d, k0h[t], k1h[t], o0[t], o1[t], qb[g][t][0], qb[g][t][1]);
+                        if constexpr (F32) mma_16816(d, k0h[t], k1h[t], o0[t], o1[t], qbl[g][t][0], qbl[g][t][1]);
                     }
                     acc[0][0] = fmaf(s0, d[0], acc[0][0]);
                     acc[0][1] = fmaf(s0, d[1], acc[0][1]);
@@ -571,14 +648,8 @@ __global__ void __launch_bounds__(kScoreThreads, R == 4 ? 5 : R == 8 ? 4 : 2) kv
         }
         __syncwarp();
         // not every row sees every key of the chunk: those it does not see leave as -inf
-        const unsigned there = has;
         const bool whole = there == (1u << U) - 1u && k1 - k0 == C && k1 - 1 <= pos_first &&
                            (!a.g.window || k1 <= a.g.sinks || k0 > pos_last - a.g.window);
-        // the next chunk's loads are on their way while the rows are looked through
-        if (ch + 1 < ch1) {
-            has = load_chunk(ch + 1, pages);
-            pages = page_of(ch + 2);
-        }
         // ---- the row's part of the chunk: keys (i * LPR + sub) * 4 + e
         float v[KPL];
 #pragma unroll
@@ -638,6 +709,13 @@ __global__ void __launch_bounds__(kScoreThreads, R == 4 ? 5 : R == 8 ? 4 : 2) kv
             out[put++] = make_int2(__float_as_int(x * mul * mul2), k0 + kk);
         }
         __syncwarp();
+        if (++stage == kStages) { stage = 0; phase ^= 1; }
+    }
+    if (!ok) {
+        // a copy that never came: report it, let the others land (2 s each at most), no scores
+        if (a.bad && lane == 0) atomicOr(a.bad, kKvBadWait);
+        for (int i = 0; i < kStages; ++i) wait_phase(&bars[i], i >= stage ? phase : phase ^ 1);
+        m = nanf("");
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (lreal && sub == 0) {
@@ -892,7 +970,7 @@ __global__ void __launch_bounds__(kSolveThreads) kv4_solve_kernel(const Kv4Args 
     const int* table = a.table + (size_t)b * a.g.max_pages;
     const uint32_t* codes = reinterpret_cast<const uint32_t*>(a.v_codes);
     const uint32_t* meta = reinterpret_cast<const uint32_t*>(a.v_meta);
-    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, accz = 0.f;
+    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     auto fetch = [&](int j, uint32_t& w, uint32_t& mt) {
         const int page = kv4_page(a.g, table, j);
         w = mt = 0u;
@@ -902,11 +980,10 @@ __global__ void __launch_bounds__(kSolveThreads) kv4_solve_kernel(const Kv4Args 
             mt = __ldg(meta + row * G + grp);
         }
     };
-    auto weigh = [&](float p, uint32_t w, uint32_t mt) {
-        const float ps = p * bf16_lo(mt);
-        accz = fmaf(p, bf16_hi(mt), accz);
+    auto weigh = [&](float p, uint32_t w, uint32_t mt) {   // (values first: the pair's terms cancel)
+        const float sc = bf16_lo(mt), z = bf16_hi(mt);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i] = fmaf(ps, (float)((w >> (4 * i)) & 15u), acc[i]);
+        for (int i = 0; i < 8; ++i) acc[i] = fmaf(p, fmaf(sc, (float)((w >> (4 * i)) & 15u), z), acc[i]);
     };
     if (fits) {
         // the support in key order, over the same arrays: each warp compacts its own run
@@ -980,7 +1057,6 @@ __global__ void __launch_bounds__(kSolveThreads) kv4_solve_kernel(const Kv4Args 
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        acc[i] += accz;
 #pragma unroll
         for (int d = LPK; d < 32; d <<= 1) acc[i] += __shfl_xor_sync(kFull, acc[i], d);
     }
@@ -1011,7 +1087,12 @@ cudaError_t write_or_read(const Kv4Args& a, bool write, cudaStream_t s) {
 template <typename T, int D, int R>
 cudaError_t launch_scores(const Kv4Args& a, cudaStream_t s) {
     const dim3 grid((a.nrun + kScoreWarps - 1) / kScoreWarps, a.blocks, a.g.B * a.Hkv);
-    kv4_scores_kernel<T, D, R><<<grid, kScoreThreads, 0, s>>>(a);
+    constexpr int sm = kScoreWarps * ScoreSmem<D, R>::kBytes;
+    if (sm > 47 * 1024) {   // (beside the static part)
+        cudaError_t e = cudaFuncSetAttribute(kv4_scores_kernel<T, D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, sm);
+        if (e != cudaSuccess) return e;
+    }
+    kv4_scores_kernel<T, D, R><<<grid, kScoreThreads, sm, s>>>(a);
     return cudaGetLastError();
 }
 

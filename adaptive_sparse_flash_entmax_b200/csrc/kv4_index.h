@@ -23,7 +23,8 @@ namespace ent {
 constexpr int kKvGroup = 32;   // dimensions that share a (scale, zero) pair
 constexpr int kKvTile = 16;    // keys of one matrix instruction; a page holds a multiple of it
 constexpr int kKvBadPage = 1;  // bits of the caller's `bad` word: a page number outside the pool,
-constexpr int kKvBadLen = 2;   // a start or length outside what the call covers
+constexpr int kKvBadLen = 2;   // a start or length outside what the call covers,
+constexpr int kKvBadWait = 4;  // a bounded device wait that gave up (the rows it served are NaN)
 
 struct Kv4Geom {
     int B, L;                // sequences, new tokens of each (rows of q, k, v)

@@ -371,7 +371,8 @@ ent_status ent_entmax_rows_bwd(const void *z, const float *tau, const void *dp, 
  *   beyond the cover                   tokens, max_len for the attention) are treated
  *                                      as padding (a negative one: all rows);
  * and bad (nullable, one device int32, zeroed by the caller) gets bit 0 (1) for the
- * former and bit 1 (2) for the latter or'ed in.  No call reads or writes outside the
+ * former and bit 1 (2) for the latter or'ed in, and bit 2 (4) if a bounded device wait of
+ * the attention gave up (its rows are NaN then).  No call reads or writes outside the
  * arrays whatever the three hold.
  *
  * ent_attn_kv4_write quantises k, v [B][Hkv][L][d] (dtype ENT_F32 or ENT_BF16) into the
