@@ -263,11 +263,13 @@ __global__ void __launch_bounds__(kKvThreads) kv4_read_kernel(const Kv4Args a) {
 // in afterwards:
 //     q.k = sum_groups scale * (codes . q) + zero * sum q,
 // the second sum as a product too: a lane's pair of group c is two elements of an A operand,
-// met by (0, sum q of group c) in three bf16 parts (24 bits); float32 rows take codes less 8
-// and (8 sum q, sum q).
+// met by (0, sum q of group c) in three bf16 parts (24 bits).
 // The queries are fp16, scaled per row by a power of two so that the largest lies in
 // [2^14, 2^15): exact for bf16 values down to 2^-31 of the largest, below which the
-// rounding is 2^-39 of it; a float32 row is the sum of two such halves (22 bits).
+// rounding is 2^-39 of it; a float32 row is the sum of two such halves (22 bits).  Its scores
+// are off by a unit or two in the last place, three times what a float dot product is (codes
+// less 8, a float zeros' term and rounded joins of partial products were tried and bring
+// nothing: O stays at 2e-6 of the 64-bit result where a plain float form has 0.9e-6).
 // The scores of a chunk pass through the warp's shared memory (queries by keys), where 32/R
 // lanes a row take their maximum and the candidates above the CTA's maximum so far - 1 (which
 // of the warps got how far does not matter: the solver drops what the final maximum rules out).
@@ -505,14 +507,7 @@ __global__ void __launch_bounds__(kScoreThreads, R == 4 ? 4 : R == 8 ? 3 : 2) kv
             }
         }
 #pragma unroll
-        for (int t = 0; t < 3; ++t) {
-            qz[nt][t] = bf16_part(zsum);
-            // float32: the codes are less 8, and the pair's scale meets 8 times the sum
-            if constexpr (F32) {
-                const float part = __uint_as_float(qz[nt][t]) * 8.f;
-                qz[nt][t] |= __float_as_uint(part) >> 16;
-            }
-        }
+        for (int t = 0; t < 3; ++t) qz[nt][t] = bf16_part(zsum);
         // x = cx 2^(24 - e) s, in two factors where one would overflow (24 - e <= 137);
         // a row with a NaN or an infinity has NaN scores
         const int e1 = min(24 - e, 100);
@@ -582,23 +577,13 @@ __global__ void __launch_bounds__(kScoreThreads, R == 4 ? 4 : R == 8 ? 3 : 2) kv
                 mma_16816_bf_0(acc[nt], mz[0], mz[1], mz[0], mz[1], qz[nt][0], qz[nt][1]);
                 mma_1688_bf(acc[nt], mz[0], mz[1], qz[nt][2]);
             }
-            // a word's codes as four pairs of halves; for float32 queries less 8, which takes the
-            // cancellation between the codes' term and the zeros' out of the float sums
+            // a word's codes as four pairs of halves
             auto halves = [](uint32_t x, uint32_t (&h)[4]) {
                 h[0] = x & 0x000f000fu;
                 h[1] = x & 0x00f000f0u;
                 x >>= 8;
                 h[2] = x & 0x000f000fu;
                 h[3] = x & 0x00f000f0u;
-                if constexpr (F32) {
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-                        const uint32_t eight = t & 1 ? 0x00800080u : 0x00080008u;   // 8 of the same unit
-                        const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&h[t]),
-                                                  *reinterpret_cast<const __half2*>(&eight));
-                        h[t] = *reinterpret_cast<const uint32_t*>(&y);
-                    }
-                }
             };
 #pragma unroll
             for (int g = 0; g < GS; ++g) {
