@@ -324,12 +324,19 @@ __device__ __forceinline__ void load_words(const char* p, uint32_t (&w)[G]) {
 }
 
 // `bytes` (a multiple of 16, as both addresses) from this GPU's memory into shared memory,
-// counted at `bar`
-__device__ __forceinline__ void bulk_copy(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-    asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                     tc::smem_u32(dst)),
-                 "l"(src), "r"(bytes), "r"(tc::smem_u32(bar))
-                 : "memory");
+// counted at `bar`; first to leave the L2 cache: the keys pass through once, and the candidates
+// that the solver reads next are to stay.
+__device__ __forceinline__ uint64_t evict_first() {
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+__device__ __forceinline__ void bulk_copy(void* dst, const void* src, uint32_t bytes, uint64_t* bar, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
+            tc::smem_u32(dst)),
+        "l"(src), "r"(bytes), "r"(tc::smem_u32(bar)), "l"(policy)
+        : "memory");
 }
 
 // Waits for a phase, 2 s at most.
@@ -416,6 +423,7 @@ __global__ void __launch_bounds__(kScoreThreads, R == 4 ? 4 : R == 8 ? 3 : 2) kv
     // Starts the copies of a chunk into its stage, a tile a lane; what is not there is not
     // copied, and no row sees it.  `has`: four bits a stage, the tiles that are there.
     unsigned has = 0;
+    const uint64_t policy = evict_first();
     int next_stage = 0, pages = page_of(ch0);
     auto issue = [&](int ch) {
         const unsigned there = __ballot_sync(kFull, pages >= 0);
@@ -426,9 +434,9 @@ __global__ void __launch_bounds__(kScoreThreads, R == 4 ? 4 : R == 8 ? 3 : 2) kv
             char* dst = ring + next_stage * L::kStage;
             const size_t row = kv4_row(a.g, a.Hkv, pages, hk, first_key(ch) + lane * kKvTile);
             bulk_copy(dst + lane * kKvTile * kTokenB, reinterpret_cast<const char*>(a.k_codes) + row * kTokenB,
-                      kKvTile * kTokenB, bar);
+                      kKvTile * kTokenB, bar, policy);
             bulk_copy(dst + L::kCodes + lane * kKvTile * kMetaB, reinterpret_cast<const char*>(a.k_meta) + row * kMetaB,
-                      kKvTile * kMetaB, bar);
+                      kKvTile * kMetaB, bar, policy);
         }
         has = (has & ~(15u << (4 * next_stage))) | there << (4 * next_stage);
         next_stage = next_stage + 1 == kStages ? 0 : next_stage + 1;
@@ -667,7 +675,9 @@ __global__ void __launch_bounds__(kScoreThreads, R == 4 ? 4 : R == 8 ? 3 : 2) kv
         for (int o = 1; o < LPR; o <<= 1) m = max_nan(m, __shfl_xor_sync(kFull, m, o));
         if (sub == 0) *const_cast<volatile float*>(&row_max[lrow]) = m;
         // above m - 1, and the maximum itself: where |m| >= 2^24 makes them equal, the limit is
-        // the next float below m (m = -inf or NaN: it is NaN, and nothing is above)
+        // the next float below m (m = -inf or NaN: it is NaN, and nothing is above).  (A higher
+        // bound of tau, proved by the run's own keys, halves the candidates of a run of 20 chunks
+        // and costs as much as they do.)
         float lim = m - 1.f;
         if (!(lim < m)) lim = __int_as_float(__float_as_int(m) + (m > 0.f ? -1 : 1));
         unsigned take = 0;
@@ -745,7 +755,7 @@ __device__ __forceinline__ int warps_before(int n, int* box, int* all) {
 }
 
 template <typename T, int D, int GM>
-__global__ void __launch_bounds__(kSolveThreads) kv4_solve_kernel(const Kv4Args a) {
+__global__ void __launch_bounds__(kSolveThreads, 4) kv4_solve_kernel(const Kv4Args a) {
     constexpr int G = D / kKvGroup, LPK = D / 8, KPW = 32 / LPK;
     extern __shared__ int solve_smem[];
     float* ys = reinterpret_cast<float*>(solve_smem);   // [kCap] x - m of the candidates, then their weights
@@ -754,7 +764,7 @@ __global__ void __launch_bounds__(kSolveThreads) kv4_solve_kernel(const Kv4Args 
     __shared__ float red[3][kSolveWarps];
     __shared__ int box[kSolveWarps], box2[kSolveWarps];
     __shared__ float bc[2];
-    __shared__ float part[kSolveWarps][D];
+    __shared__ float halves[kSolveWarps][D];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = a.g.L * a.group;    // rows of one key head
     const int bk = blockIdx.x / per, r = blockIdx.x - bk * per;
@@ -814,77 +824,68 @@ __global__ void __launch_bounds__(kSolveThreads) kv4_solve_kernel(const Kv4Args 
     if (tid == 0) off[nrun] = raw;
     __syncthreads();
 
-    // ---- candidates above m - 1, in order, into shared memory: each warp takes its part of all
-    // runs' entries as one sequence.  Where the sequence fits, the kept ones stay within the
-    // warp's part of the arrays; else they are counted first and then placed.
-    const bool direct = raw <= kCap;
-    const int part0 = (int)((long long)raw * warp / kSolveWarps), part1 = (int)((long long)raw * (warp + 1) / kSolveWarps);
-    // calls f(y, key, lanes that keep theirs) for 32 entries of the part at a time
-    auto each = [&](auto f) {
-        int i = 0;   // the run that holds entry part0 (by halving), then forward
+    // ---- tau - m over what `each_y` goes through, n keys at most
+    const float gamma = a.gamma;
+    RowSolver sv;
+    auto solve = [&](int n, float lo, auto each_y) {
+        sv.done = 0;
+        sv.iters = 0;
+        sv.lo = lo;
+        sv.hi = fmaxf(lo, -exp2f((1.f - a.alpha) * __log2f((float)n)) + 1e-6f);
+        sv.tau = 0.5f * (sv.lo + sv.hi);
+        for (int pass = 1;; ++pass) {
+            float F0 = 0.f, F1 = 0.f, F2 = 0.f;
+            each_y([&](float y) {
+                float t0, t1, t2;
+                entmax_terms_bf<GM>(y - sv.tau, gamma, t0, t1, t2);
+                F0 += t0; F1 += t1; F2 += t2;
+            });
+            F0 = warp_sum(F0); F1 = warp_sum(F1); F2 = warp_sum(F2);
+            if (lane == 0) { red[0][warp] = F0; red[1][warp] = F1; red[2][warp] = F2; }
+            __syncthreads();
+            if (tid == 0) {
+                F0 = F1 = F2 = 0.f;
+                for (int w = 0; w < kSolveWarps; ++w) { F0 += red[0][w]; F1 += red[1][w]; F2 += red[2][w]; }
+                solver_update(sv, F0, F1, F2, gamma, gamma == 1.f, pass, kKvFtol, kKvStol);
+                bc[0] = sv.tau;
+                bc[1] = sv.done ? 1.f : 0.f;
+            }
+            __syncthreads();
+            sv.tau = bc[0];
+            if (bc[1] != 0.f) break;
+        }
+    };
+
+    // ---- candidates above a bound of tau, in order, into shared memory.  All runs' entries are
+    // one sequence, of which each warp takes an equal part.
+    // calls f(y, key, is there) for 32 of the entries [from, to) at a time
+    auto each = [&](int from, int to, auto f) {
+        int i = 0;   // the run that holds the first entry (by halving), then forward
 #pragma unroll 1
         for (int step = kKvMaxRuns / 2; step > 0; step >>= 1)
-            if (i + step < nrun && off[i + step] <= part0) i += step;
+            if (i + step < nrun && off[i + step] <= from) i += step;
         constexpr int U = 4;
 #pragma unroll 1
-        for (int base = part0; base < part1; base += 32 * U) {
+        for (int base = from; base < to; base += 32 * U) {
             int2 c[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int e = base + u * 32 + lane;
                 c[u] = make_int2(0, -1);
-                if (e < part1) {
+                if (e < to) {
                     while (off[i + 1] <= e) ++i;
                     c[u] = list_of(i)[e - off[i]];
                 }
             }
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const float y = __int_as_float(c[u].x) - m;
-                const bool take = c[u].y >= 0 && y > -1.f;
-                f(y, c[u].y, take, __ballot_sync(kFull, take));
-            }
+            for (int u = 0; u < U; ++u) f(__int_as_float(c[u].x) - m, c[u].y, c[u].y >= 0);
         }
     };
-    int e0 = part0, mine = 0, total = 0;
-    bool fits = true;
-    if (!direct) {
-        each([&](float, int, bool, unsigned mask) { mine += __popc(mask); });
-        e0 = warps_before(mine, box, &total);
-        fits = total <= kCap;
-        mine = 0;
-    }
-    if (fits)
-        each([&](float y, int j, bool take, unsigned mask) {
-            if (take) {
-                const int p = e0 + mine + __popc(mask & ((1u << lane) - 1u));
-                ys[p] = y;
-                js[p] = j;
-            }
-            mine += __popc(mask);
-        });
-    else
-        // each warp closes up its own lists in the workspace, so that what follows does not
-        // depend on what else the scores kernel left in them
-        for (int i = c0; i < c1; ++i) {
-            int2* list = list_of(i);
-            const int n = off[i + 1] - off[i];
-            int kept = 0;
-            for (int b0 = 0; b0 < n; b0 += 32) {
-                const int e = b0 + lane;
-                const int2 c = e < n ? list[e] : make_int2(0, -1);
-                const bool take = c.y >= 0 && __int_as_float(c.x) - m > -1.f;
-                const unsigned mask = __ballot_sync(kFull, take);
-                if (take) list[kept + __popc(mask & ((1u << lane) - 1u))] = c;
-                kept += __popc(mask);
-                __syncwarp();
-            }
-            __syncwarp();
-            if (lane == 0) cn[i] = kept;
-            __syncwarp();
-        }
-    // entry i of all warps' runs in order: which of them lie where depends on the raw counts, but
-    // not the sequence of entries, so sums over i are the same from call to call
+    auto part = [&](int n, int w) { return (int)((long long)n * w / kSolveWarps); };
+    // Kept entries lie in each warp's own part of the arrays, from e0 on.  Entry i of all parts in
+    // order: which part it lies in depends on the raw counts, but not the sequence of entries, so
+    // sums over i are the same from call to call.
+    int e0 = 0, mine = 0;
     int ends[kSolveWarps], from[kSolveWarps];
     auto close_up = [&](int n) {
         __syncthreads();
@@ -906,24 +907,79 @@ __global__ void __launch_bounds__(kSolveThreads) kv4_solve_kernel(const Kv4Args 
             if (i >= ends[k]) f = from[k + 1];
         return f + i;
     };
-    const int all = close_up(mine);
-    if (fits) total = all;
-
-    // ---- tau - m
-    const float gamma = a.gamma;
-    RowSolver sv;
-    sv.done = 0;
-    sv.iters = 0;
-    sv.lo = -1.f;
-    sv.hi = fmaxf(-1.f, -exp2f((1.f - a.alpha) * __log2f((float)total)) + 1e-6f);
-    sv.tau = 0.5f * (sv.lo + sv.hi);
-    for (int pass = 1;; ++pass) {
-        float F0 = 0.f, F1 = 0.f, F2 = 0.f;
-        auto add = [&](float y) {
-            float t0, t1, t2;
-            entmax_terms_bf<GM>(y - sv.tau, gamma, t0, t1, t2);
-            F0 += t0; F1 += t1; F2 += t2;
+    // the entries of the first n that lie above `bound`; false where they do not fit
+    auto gather = [&](int n, float bound, int* total) {
+        const int p0 = part(n, warp), p1 = part(n, warp + 1);
+        auto place = [&](int room) {
+            mine = 0;
+            each(p0, p1, [&](float y, int j, bool there) {
+                const bool take = there && y > bound;
+                const unsigned mask = __ballot_sync(kFull, take);
+                const int p = mine + __popc(mask & ((1u << lane) - 1u));
+                if (take && p < room) {
+                    ys[e0 + p] = y;
+                    js[e0 + p] = j;
+                }
+                mine += __popc(mask);
+            });
         };
+        // where all would fit, each warp has the room; else an equal share, and if that was too
+        // little for one of them, what they counted
+        const int room = n <= kCap ? p1 - p0 : kCap / kSolveWarps;
+        e0 = n <= kCap ? p0 : warp * room;
+        place(room);
+        if (__syncthreads_or(mine > room)) {
+            e0 = warps_before(mine, box, total);
+            if (*total > kCap) return false;
+            place(mine);
+        }
+        *total = close_up(mine);
+        return true;
+    };
+    // tau > m - 1.  Where there are far more entries than fit, tau also lies above the tau of
+    // fewer keys: of the first runs that surely fit, then of eight times as many above that, and
+    // so on (with the dense weights of alpha 1.25 the first drops nine candidates of ten; without
+    // it a sequence of 100000 keys takes 710 us instead of 470, in passes over its lists; below
+    // 4 kCap entries most of which lie under m - 1, it costs 12 us of 108).
+    float bound = -1.f;
+    int total = 0;
+    bool fits = true;
+    for (int runs = raw <= 4 * kCap ? nrun : max(1, kCap / stride);; runs = runs > nrun / 8 ? nrun : runs * 8) {
+        fits = gather(off[min(runs, nrun)], bound, &total);
+        if (runs >= nrun) break;
+        if (!fits || total == 0) continue;   // (no key of the first runs may be near m)
+        solve(total, -1.f, [&](auto add) {
+            for (int i = tid; i < total; i += kSolveThreads) add(ys[where(i)]);
+        });
+        bound = fmaxf(bound, sv.tau - 2e-6f);   // (it stops within 2e-7 of the sum, a step of it at most)
+        __syncthreads();
+    }
+    if (!fits) {
+        // scores too equal: the lists stay in the workspace, closed up so that what follows does
+        // not depend on what else the scores kernel left in them
+        mine = 0;
+        for (int i = c0; i < c1; ++i) {
+            int2* list = list_of(i);
+            const int n = off[i + 1] - off[i];
+            int kept = 0;
+            for (int b0 = 0; b0 < n; b0 += 32) {
+                const int e = b0 + lane;
+                const int2 c = e < n ? list[e] : make_int2(0, -1);
+                const bool take = c.y >= 0 && __int_as_float(c.x) - m > bound;
+                const unsigned mask = __ballot_sync(kFull, take);
+                if (take) list[kept + __popc(mask & ((1u << lane) - 1u))] = c;
+                kept += __popc(mask);
+                __syncwarp();
+            }
+            __syncwarp();
+            if (lane == 0) cn[i] = kept;
+            __syncwarp();
+            mine += kept;
+        }
+        total = close_up(mine);
+    }
+
+    solve(total, -1.f, [&](auto add) {
         if (fits) {
             for (int i = tid; i < total; i += kSolveThreads) add(ys[where(i)]);
         } else {
@@ -933,20 +989,7 @@ __global__ void __launch_bounds__(kSolveThreads) kv4_solve_kernel(const Kv4Args 
                 for (int e = lane; e < n; e += 32) add(__int_as_float(list[e].x) - m);
             }
         }
-        F0 = warp_sum(F0); F1 = warp_sum(F1); F2 = warp_sum(F2);
-        if (lane == 0) { red[0][warp] = F0; red[1][warp] = F1; red[2][warp] = F2; }
-        __syncthreads();
-        if (tid == 0) {
-            F0 = F1 = F2 = 0.f;
-            for (int w = 0; w < kSolveWarps; ++w) { F0 += red[0][w]; F1 += red[1][w]; F2 += red[2][w]; }
-            solver_update(sv, F0, F1, F2, gamma, gamma == 1.f, pass, kKvFtol, kKvStol);
-            bc[0] = sv.tau;
-            bc[1] = sv.done ? 1.f : 0.f;
-        }
-        __syncthreads();
-        sv.tau = bc[0];
-        if (bc[1] != 0.f) break;
-    }
+    });
     if (tid == 0 && a.tau) a.tau[orow] = sv.tau + m;
 
     // ---- O over the support
@@ -1048,13 +1091,13 @@ __global__ void __launch_bounds__(kSolveThreads) kv4_solve_kernel(const Kv4Args 
     if (slot == 0) {
         // word t = c G + w holds dimensions 32 w + 8 c ..
 #pragma unroll
-        for (int i = 0; i < 8; ++i) part[warp][32 * (t % G) + 8 * (t / G) + i] = acc[i];
+        for (int i = 0; i < 8; ++i) halves[warp][32 * (t % G) + 8 * (t / G) + i] = acc[i];
     }
     __syncthreads();
     for (int i = tid; i < D; i += kSolveThreads) {
         float v = 0.f;
 #pragma unroll
-        for (int w = 0; w < kSolveWarps; ++w) v += part[w][i];
+        for (int w = 0; w < kSolveWarps; ++w) v += halves[w][i];
         store_f(o, i, v);
     }
 }
