@@ -105,7 +105,8 @@ def kv4_write(cache, k, v, block_table, start, new_lens=None, *, bad=None) -> No
     """Quantise k, v [B, Hkv, L, d] into the cache at positions start .. start + new_lens - 1.
 
     ``bad`` (int32 [1], zeroed by the caller) gets bit 0 set where a page number lies outside the pool,
-    bit 1 where a start or length lies outside the table; the rows concerned are not written.  Pages
+    bit 1 where a start or length lies outside the table; the rows concerned are not written (and in the
+    attention bit 2 if a bounded device wait gave up).  Pages
     being written must belong to one sequence."""
     _check_rows4(k, v)
     B, H, L, d = k.shape
@@ -135,19 +136,36 @@ def kv4_read(cache, block_table, start, n: int, new_lens=None, *, dtype=torch.bf
         if k.shape != (B, heads, n, d):
             raise ValueError(f"out must be of shape {(B, heads, n, d)}, not {tuple(k.shape)}")
     _check_rows4(k, v)
+    if k.device != device:
+        raise ValueError("out must be on the device of the other tensors")
     table, st, nl, bp, max_pages = _check_seqs(block_table, start, new_lens, bad, B, device)
     _call(capi.ent_attn_kv4_read, device, *(t.data_ptr() for t in cache), pages, page, table, max_pages,
           st, nl, B, heads, n, d, _DTYPES[k.dtype], k.data_ptr(), v.data_ptr(), bp)
     return k, v
 
 
+def _cover(window, sinks, max_len, cap):
+    """(window, sinks, max_len) as the library takes them: window 0 for none, all within 31 bits."""
+    if window is None:
+        if sinks:
+            raise ValueError("sinks need a window")
+        window = 0
+    elif window < 1 or sinks < 0:
+        raise ValueError(f"window must be at least 1 and sinks at least 0, not {window} and {sinks}")
+    if max_len is None:
+        max_len = cap
+    elif not 0 <= max_len <= cap:
+        raise ValueError(f"max_len must lie in 0 .. {cap} (what the block table covers), not {max_len}")
+    big = 2 ** 31 - 1
+    return min(window, big), min(sinks, big), max_len
+
+
 def kv4_workspace(q, cache, block_table, *, window: int | None = None, sinks: int = 0,
                   max_len: int | None = None) -> torch.Tensor:
     """A workspace for ``entmax_attn_kv4`` of these arguments; it serves one call at a time."""
     B, Hq, L, d = q.shape
-    cap = block_table.shape[1] * cache[0].shape[2]
-    n = _workspace_size(B, Hq, cache[0].shape[1], L, d, _DTYPES[q.dtype], cap if max_len is None else max_len,
-                        window or 0, sinks)
+    window, sinks, max_len = _cover(window, sinks, max_len, block_table.shape[1] * cache[0].shape[2])
+    n = _workspace_size(B, Hq, cache[0].shape[1], L, d, _DTYPES[q.dtype], max_len, window, sinks)
     return torch.empty(max(n, 256), dtype=torch.uint8, device=q.device)
 
 
@@ -167,15 +185,8 @@ def entmax_attn_kv4(q, cache, block_table, start, alpha: float = 1.5, *, new_len
     pages, heads, page, dc = _check_cache(cache, device)
     if dc != d or Hq % heads:
         raise ValueError(f"the cache holds {heads} heads of {dc}; q has {Hq} of {d}")
-    if window is None:
-        if sinks:
-            raise ValueError("sinks need a window")
-        window = 0
-    elif window < 1 or sinks < 0:
-        raise ValueError(f"window must be at least 1 and sinks at least 0, not {window} and {sinks}")
+    window, sinks, max_len = _cover(window, sinks, max_len, block_table.shape[-1] * page)
     table, st, nl, bp, max_pages = _check_seqs(block_table, start, new_lens, bad, B, device)
-    if max_len is None:
-        max_len = max_pages * page
     dt = _DTYPES[q.dtype]
     if out is None:
         out = torch.empty_like(q)

@@ -199,6 +199,21 @@ def test_attention_more_candidates_than_shared_memory(alpha):
     check(q, cache, tables(1, max_pages, max_pages, gen), [n - 2], None, alpha, 0, 0, page, "f32")
 
 
+@pytest.mark.parametrize("alpha,spread", [(1.25, 1.0), (1.25, 1e-4), (2.0, 0.05)])
+def test_attention_many_candidates(alpha, spread):
+    """40000 keys, most of them within 1 of the maximum: the solver bounds tau by fewer keys first; with nearly
+    equal scores nothing fits all the same.  The same result every time."""
+    gen = torch.Generator().manual_seed(17)
+    d, page, n = 32, 128, 40000
+    max_pages = -(-n // page)
+    cache = pool(max_pages, 1, page, d, gen)
+    table = tables(1, max_pages, max_pages, gen)
+    q = (spread * torch.randn(1, 2, 1, d, generator=gen)).cuda()
+    o = check(q, cache, table, [n - 1], None, alpha, 0, 0, page, "f32")
+    for _ in range(3):
+        assert torch.equal(entmax_attn_kv4(q, cache, table.cuda(), i32([n - 1]), alpha), o)
+
+
 def test_attention_large_scores():
     """Scores far beyond 2^24 apart and from zero: the largest takes all."""
     gen = torch.Generator().manual_seed(10)
@@ -268,6 +283,23 @@ def test_bad_pages_and_lengths():
     bad.zero_()
     k, v = kv4_read(cache, i32([[0, 99, 1]]), i32([10]), 20, dtype=torch.float32, bad=bad)
     assert int(bad) == 1 and bool(k[:, :, :6].all()) and not bool(k[:, :, 6:].any()) and not bool(v[:, :, 6:].any())
+
+
+def test_cover_arguments():
+    """A window or sinks beyond 31 bits are the sequence; a cover beyond the table is refused."""
+    gen = torch.Generator().manual_seed(18)
+    cache = pool(4, 1, 16, 64, gen)
+    table, q = i32([[0, 1, 2, 3]]), torch.randn(1, 2, 1, 64, generator=gen).cuda()
+    want = entmax_attn_kv4(q, cache, table, i32([50]), 1.5)
+    assert torch.equal(entmax_attn_kv4(q, cache, table, i32([50]), 1.5, window=2 ** 40, sinks=2 ** 33), want)
+    assert torch.equal(entmax_attn_kv4(q, cache, table, i32([50]), 1.5, max_len=51), want)
+    for kw in (dict(max_len=65), dict(max_len=-1), dict(window=0), dict(sinks=1), dict(window=3, sinks=-1)):
+        with pytest.raises(ValueError):
+            entmax_attn_kv4(q, cache, table, i32([50]), 1.5, **kw)
+        with pytest.raises(ValueError):
+            kv4_workspace(q, cache, table, **kw)
+    with pytest.raises(ValueError):
+        kv4_read(cache, table, i32([0]), 4, out=(torch.empty(1, 1, 4, 64), torch.empty(1, 1, 4, 64)))
 
 
 def test_no_cover():
