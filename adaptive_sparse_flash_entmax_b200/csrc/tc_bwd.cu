@@ -131,7 +131,9 @@ struct DqLayout {
 };
 
 // WIN (both kernels): a sliding window with sinks; the forward's block mask holds none of the
-// blocks outside it, and the blocks across its borders mask their elements here.
+// blocks outside it, and the blocks across its borders mask their elements here (dq by a 64-bit
+// word of columns: with a comparison for each border it spilled and took 193 us instead of 150
+// at B8 H12 N2048 d64, window 512; dkv 158).
 template <int D, int GM, bool WIN>
 __global__ void __launch_bounds__(kThreads, 1)
 tc_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,

@@ -157,7 +157,9 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
 // otilde = G.V / sum_j g, from which the backward takes delta without a pass over the keys.
 // WIN: a sliding window with sinks.  The tile's visible key blocks are known before the
 // first pass, so pass 0 takes them from the job list as a pass after the bound pass does;
-// blocks outside it keep block maxima of -inf and are never candidates.
+// blocks outside it keep block maxima of -inf and are never candidates.  B8 H12 N2048 d64,
+// window 512, 4 sinks: 427 us (5 blocks and 3.4 solver passes a tile, 41 us a tile: each pass
+// is three jobs long, so its latencies bound it, tensor pipe 14 %).
 template <int D, int GM, bool OT, bool WIN>
 __global__ void __launch_bounds__(kThreads, 1)
 tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,

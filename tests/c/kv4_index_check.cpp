@@ -43,6 +43,11 @@ int main() {
                                 for (int c = 0; c < n; ++c) {
                                     int k0, k1;
                                     kv4_chunk(g, s, C, c, &k0, &k1);
+                                    // the kernel's form of it
+                                    const int ns = kv4_sink_chunks(g, C), base = kv4_base(g, s.start) - ns * C;
+                                    const int f0 = c * C + (c < ns ? 0 : base);
+                                    const int f1 = kv4_min(f0 + C, c < ns ? kv4_min(kv4_sink_end(g), s.end) : s.end);
+                                    CHECK(k0 >= k1 ? f0 >= f1 : f0 == k0 && f1 == k1);
                                     if (k0 >= k1) continue;
                                     CHECK(k0 >= 0 && k1 <= s.end && k1 - k0 <= C && k0 % kKvTile == 0);
                                     for (int j = k0; j < k1; ++j) ++hits[j];
