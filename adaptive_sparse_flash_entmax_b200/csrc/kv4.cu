@@ -11,7 +11,7 @@
 // below such a maximum - 1 has p = 0: the scores never leave the chip but for the few that
 // can weigh, and value rows without a weight are never read.
 //
-// 16 sequences of 16k to 32k tokens, 32 query and 8 key heads of 128 (B200): 99 us a call for
+// 16 sequences of 16k to 32k tokens, 32 query and 8 key heads of 128 (B200): 104 us a call for
 // 253 MB of keys and weighed values, 39 at the copy rate; the scores kernel takes 78 of them,
 // bound by its instructions (half of the issue slots at four warps a scheduler; matrix pipe
 // 22 %, 3.2 TB/s), the solver the rest after it.
@@ -273,10 +273,11 @@ __global__ void __launch_bounds__(kKvThreads) kv4_read_kernel(const Kv4Args a) {
 // met by (0, sum q of group c) in three bf16 parts (24 bits).
 // The queries are fp16, scaled per row by a power of two so that the largest lies in
 // [2^14, 2^15): exact for bf16 values down to 2^-31 of the largest, below which the
-// rounding is 2^-39 of it; a float32 row is the sum of two such halves (22 bits).  Its scores
-// are off by a unit or two in the last place, three times what a float dot product is (codes
-// less 8, a float zeros' term and rounded joins of partial products were tried and bring
-// nothing: O stays at 2e-6 of the 64-bit result where a plain float form has 0.9e-6).
+// rounding is 2^-39 of it; a float32 row is the sum of two such halves (22 bits).  Float32
+// scores are then off by what the product truncates, about 2^-24 of its largest term for each
+// of 16: O is at 2e-6 to 3e-6 of the 64-bit result where a plain float form has 0.5e-6 to
+// 0.9e-6 (codes less 8, a float zeros' term and rounded joins of the partial products were
+// tried and bring nothing).
 // The scores of a chunk pass through the warp's shared memory (queries by keys), where 32/R
 // lanes a row take their maximum and the candidates above the CTA's maximum so far - 1 (which
 // of the warps got how far does not matter: the solver drops what the final maximum rules out).
@@ -733,7 +734,7 @@ __global__ void __launch_bounds__(kScoreThreads, R == 4 ? 4 : R == 8 ? 3 : 2) kv
 // keys weigh), and O accumulates over the support, D/8 lanes per value row.  Scores are held
 // relative to m, so tau keeps its precision for scores of any size.  Every sum has a fixed
 // order: the result does not change from run to run.  A row with more than kCap candidates
-// even above m - 1 goes over the runs' lists again in every pass.
+// above what is known to lie below tau goes over the runs' lists again in every pass.
 constexpr int kSolveThreads = 256;
 constexpr int kSolveWarps = kSolveThreads / 32;
 constexpr int kCap = 4096;
@@ -794,7 +795,7 @@ __global__ void __launch_bounds__(kSolveThreads, 4) kv4_solve_kernel(const Kv4Ar
     auto list_of = [&](int i) { return cand + (size_t)i * stride; };
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
-    // ---- row maximum (every warp for itself), then the runs' offsets, a quarter each warp
+    // ---- row maximum (every warp for itself), then the runs' offsets, a share each warp
     float m = -INFINITY;
     bool nan = false;
     for (int i = lane; i < nrun; i += 32) {
