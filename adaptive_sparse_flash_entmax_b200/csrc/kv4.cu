@@ -410,18 +410,14 @@ __global__ void __launch_bounds__(kScoreThreads, R == 4 ? 4 : R == 8 ? 3 : 2) kv
     }
     __syncwarp();
 
-    // chunk ch holds keys k0 .. k1-1 (kv4_chunk, with what does not change taken out)
     const int* table = a.table + (size_t)b * a.g.max_pages;
-    const int ns = kv4_sink_chunks(a.g, C), sink_end = kv4_min(kv4_sink_end(a.g), s.end);
-    const int base = kv4_base(a.g, s.start) - ns * C;
-    auto first_key = [&](int ch) { return ch * C + (ch < ns ? 0 : base); };
-    auto end_key = [&](int ch, int k0) { return kv4_min(k0 + C, ch < ns ? sink_end : s.end); };
+    const Kv4Chunks chunks(a.g, s, C);
     // page of tile `lane` of a chunk (lanes below U)
     auto page_of = [&](int ch) {
         int p = -1;
         if (ch < ch1 && lane < U) {
-            const int k0 = first_key(ch), kb = k0 + lane * kKvTile;
-            if (kb < end_key(ch, k0)) {
+            const int kb = chunks.first(ch) + lane * kKvTile;
+            if (kb < chunks.end(ch)) {
                 p = kv4_page(a.g, table, kb);
                 if (p < 0 && a.bad) atomicOr(a.bad, kKvBadPage);
             }
@@ -440,7 +436,7 @@ __global__ void __launch_bounds__(kScoreThreads, R == 4 ? 4 : R == 8 ? 3 : 2) kv
         __syncwarp();
         if (pages >= 0) {
             char* dst = ring + next_stage * L::kStage;
-            const size_t row = kv4_row(a.g, a.Hkv, pages, hk, first_key(ch) + lane * kKvTile);
+            const size_t row = kv4_row(a.g, a.Hkv, pages, hk, chunks.first(ch) + lane * kKvTile);
             bulk_copy(dst + lane * kKvTile * kTokenB, reinterpret_cast<const char*>(a.k_codes) + row * kTokenB,
                       kKvTile * kTokenB, bar, policy);
             bulk_copy(dst + L::kCodes + lane * kKvTile * kMetaB, reinterpret_cast<const char*>(a.k_meta) + row * kMetaB,
@@ -564,7 +560,7 @@ __global__ void __launch_bounds__(kScoreThreads, R == 4 ? 4 : R == 8 ? 3 : 2) kv
     for (int ch = ch0; ch < ch1; ++ch) {
         // (the stage of the chunk before this one, which every lane has read)
         if (ch + kStages - 1 < ch1) issue(ch + kStages - 1);
-        const int k0 = first_key(ch), k1 = end_key(ch, k0);
+        const int k0 = chunks.first(ch), k1 = chunks.end(ch);
         const unsigned there = has >> (4 * stage) & 15u;
         ok = wait_phase(&bars[stage], phase);
         if (!__all_sync(kFull, ok)) { ok = false; break; }

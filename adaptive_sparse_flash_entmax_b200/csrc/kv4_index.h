@@ -106,18 +106,16 @@ ENT_HD int kv4_seq_chunks(const Kv4Geom& g, const Kv4Seq& s, int C) {
     return kv4_sink_chunks(g, C) + (s.end > base ? (s.end - base + C - 1) / C : 0);
 }
 
-// Keys [k0, k1) of chunk c (k0 >= k1: none).
-ENT_HD void kv4_chunk(const Kv4Geom& g, const Kv4Seq& s, int C, int c, int* k0, int* k1) {
-    const int ns = kv4_sink_chunks(g, C);
-    if (c < ns) {
-        *k0 = c * C;
-        *k1 = kv4_min(kv4_min(*k0 + C, kv4_sink_end(g)), s.end);
-    } else {
-        const long long k = (long long)kv4_base(g, s.start) + (long long)(c - ns) * C;
-        *k0 = k < s.end ? (int)k : s.end;
-        *k1 = s.end - *k0 < C ? s.end : *k0 + C;
-    }
-}
+// Keys of a sequence's chunks: chunk c holds first(c) .. end(c) - 1 (none where first >= end,
+// for chunks of sinks that the sequence does not reach).
+struct Kv4Chunks {
+    int C, ns, sink_end, base, seq_end;
+    ENT_HD Kv4Chunks(const Kv4Geom& g, const Kv4Seq& s, int C_)
+        : C(C_), ns(kv4_sink_chunks(g, C_)), sink_end(kv4_min(kv4_sink_end(g), s.end)),
+          base(kv4_base(g, s.start) - ns * C_), seq_end(s.end) {}
+    ENT_HD int first(int c) const { return c * C + (c < ns ? 0 : base); }
+    ENT_HD int end(int c) const { return kv4_min(first(c) + C, c < ns ? sink_end : seq_end); }
+};
 
 // The chunks of a sequence are dealt to `nrun` runs of equal length: run i holds chunks
 // [i * kv4_run, (i + 1) * kv4_run) below kv4_seq_chunks.

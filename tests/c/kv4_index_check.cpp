@@ -41,13 +41,7 @@ int main() {
                                 CHECK(n <= kv4_chunks(g, C));
                                 std::vector<int> hits(max_len, 0);
                                 for (int c = 0; c < n; ++c) {
-                                    int k0, k1;
-                                    kv4_chunk(g, s, C, c, &k0, &k1);
-                                    // the kernel's form of it
-                                    const int ns = kv4_sink_chunks(g, C), base = kv4_base(g, s.start) - ns * C;
-                                    const int f0 = c * C + (c < ns ? 0 : base);
-                                    const int f1 = kv4_min(f0 + C, c < ns ? kv4_min(kv4_sink_end(g), s.end) : s.end);
-                                    CHECK(k0 >= k1 ? f0 >= f1 : f0 == k0 && f1 == k1);
+                                    const int k0 = Kv4Chunks(g, s, C).first(c), k1 = Kv4Chunks(g, s, C).end(c);
                                     if (k0 >= k1) continue;
                                     CHECK(k0 >= 0 && k1 <= s.end && k1 - k0 <= C && k0 % kKvTile == 0);
                                     for (int j = k0; j < k1; ++j) ++hits[j];
@@ -95,8 +89,7 @@ int main() {
         CHECK(s.rows == 3 && s.end == 1 << 30);
         const int n = kv4_seq_chunks(g, s, 512);
         CHECK(n > 0 && n <= kv4_chunks(g, 512));
-        int k0, k1;
-        kv4_chunk(g, s, 512, n - 1, &k0, &k1);
+        const int k0 = Kv4Chunks(g, s, 512).first(n - 1), k1 = Kv4Chunks(g, s, 512).end(n - 1);
         CHECK(k0 >= 0 && k0 < k1 && k1 <= s.end);
     }
     std::printf("kv4 index ok (%lld sequences)\n", cases);
