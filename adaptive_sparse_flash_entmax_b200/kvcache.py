@@ -44,36 +44,55 @@ def kv4_alloc(pages: int, heads: int, page: int, d: int, device="cuda") -> KV4Ca
                                                     ((d // _GROUP, 2), torch.bfloat16))))
 
 
+def _place(device):
+    """What get_device() gives of a tensor there (the CPU: -1)."""
+    return -1 if device.index is None else device.index
+
+
 def _check_cache(cache, device):
-    """(pages, heads, page, d) of the pool."""
+    """(pages, heads, page, d) of the pool.  (These checks are a third of a small call's host time: each
+    attribute is asked for once.)"""
     kc, km, vc, vm = cache
-    if kc.dim() != 4:
-        raise ValueError(f"expected codes [pages, heads, page, d/2], got shape {tuple(kc.shape)}")
-    pages, heads, page, half = kc.shape
+    shape = kc.shape
+    if len(shape) != 4:
+        raise ValueError(f"expected codes [pages, heads, page, d/2], got shape {tuple(shape)}")
+    pages, heads, page, half = shape
     meta = (pages, heads, page, half // 16, 2)
-    if (vc.shape != kc.shape or km.shape != meta or vm.shape != meta or kc.dtype != torch.uint8
-            or vc.dtype != torch.uint8 or km.dtype != torch.bfloat16 or vm.dtype != torch.bfloat16):
+    if not (vc.shape == shape and km.shape == meta and vm.shape == meta and kc.dtype is torch.uint8
+            and vc.dtype is torch.uint8 and km.dtype is torch.bfloat16 and vm.dtype is torch.bfloat16):
         raise ValueError("the cache must be codes uint8 [pages, heads, page, d/2] and meta bfloat16 "
                          "[pages, heads, page, d/32, 2], keys and values alike")
-    if not (kc.device == km.device == vc.device == vm.device == device):
+    where = _place(device)
+    if not (where == kc.get_device() == km.get_device() == vc.get_device() == vm.get_device()):
         raise ValueError("the cache must be on the device of the other tensors")
     if not (kc.is_contiguous() and km.is_contiguous() and vc.is_contiguous() and vm.is_contiguous()):
         raise ValueError("the cache's arrays must be contiguous")
     return pages, heads, page, 2 * half
 
 
+def _pointer(t, n, where):
+    """Device pointer of an int32 tensor of n values (None: none)."""
+    if t is None:
+        return None
+    if not (t.dtype is torch.int32 and t.shape == (n,) and t.get_device() == where
+            and t.is_contiguous()):
+        raise ValueError("start, new_lens and bad must be contiguous int32 tensors of shapes [B], [B] and [1] "
+                         "on the device of the others")
+    return t.data_ptr()
+
+
 def _check_seqs(block_table, start, new_lens, bad, B, device):
     """Device pointers (table, start, new_lens or None, bad or None) and the table's columns."""
-    if block_table.dim() != 2 or block_table.shape[0] != B:
-        raise ValueError(f"expected block_table [{B}, max_pages], got shape {tuple(block_table.shape)}")
-    for t, shape in ((block_table, block_table.shape), (start, (B,)), (new_lens, (B,)), (bad, (1,))):
-        if t is None:
-            continue
-        if t.dtype != torch.int32 or t.shape != shape or t.device != device or not t.is_contiguous():
-            raise ValueError("block_table, start, new_lens and bad must be contiguous int32 tensors of "
-                             "shapes [B, max_pages], [B], [B] and [1] on the device of the others")
-    return (block_table.data_ptr(), start.data_ptr(), new_lens.data_ptr() if new_lens is not None else None,
-            bad.data_ptr() if bad is not None else None, block_table.shape[1])
+    shape, where = block_table.shape, _place(device)
+    if len(shape) != 2 or shape[0] != B:
+        raise ValueError(f"expected block_table [{B}, max_pages], got shape {tuple(shape)}")
+    if not (block_table.dtype is torch.int32 and block_table.get_device() == where
+            and block_table.is_contiguous()):
+        raise ValueError("block_table must be a contiguous int32 tensor on the device of the others")
+    if start is None:
+        raise ValueError("start is needed")
+    return (block_table.data_ptr(), _pointer(start, B, where), _pointer(new_lens, B, where),
+            _pointer(bad, 1, where), shape[1])
 
 
 # sizes alone go in: a decoder asks with the same ones at every step

@@ -427,3 +427,33 @@ def test_prompt_then_tokens(window, sinks):
         got = torch.cat(rows[b], 1).float()
         # two routes in float (1e-4 is the float32 forward's own bound) and a rounding to bf16
         assert bool(((got - want[0]).abs() <= 1e-4 + 2.0 ** -8 * want[0].abs() * 1.01).all())
+
+
+def test_wrapper_refusals_on_the_device():
+    """Wrong shapes, types, places and layouts of the cache and of the sequences' tensors."""
+    cache = kv4_alloc(3, 2, 16, 64, "cuda")
+    x = torch.zeros(2, 2, 1, 64, device="cuda")
+    table, start = i32([[0, 1], [2, 0]]), i32([0, 0])
+    kv4_write(cache, x, x, table, start)
+    bad_caches = [cache[:1] + (cache[1].float(),) + cache[2:], (cache[0][:2],) + cache[1:],
+                  tuple(t.cpu() for t in cache), (cache[0].transpose(1, 2).contiguous().transpose(1, 2),) + cache[1:],
+                  (cache[0][0],) + cache[1:]]
+    for c in bad_caches:
+        for call in (lambda: kv4_write(c, x, x, table, start), lambda: entmax_attn_kv4(x, c, table, start),
+                     lambda: kv4_read(c, table, start, 1)):
+            with pytest.raises(ValueError):
+                call()
+    for t, s, n, b in ((table.long(), start, None, None), (table[:1], start, None, None), (table.cpu(), start, None, None),
+                       (table.t(), start, None, None), (table, start.long(), None, None), (table, start[:1], None, None),
+                       (table, start.cpu(), None, None), (table, start, i32([1]), None), (table, start, None, i32([0, 0])),
+                       (table, None, None, None)):
+        for call in (lambda: kv4_write(cache, x, x, t, s, n, bad=b),
+                     lambda: entmax_attn_kv4(x, cache, t, s, new_lens=n, bad=b)):
+            with pytest.raises(ValueError):
+                call()
+    with pytest.raises(ValueError):
+        kv4_write(cache, x[..., :32].contiguous(), x[..., :32].contiguous(), table, start)
+    with pytest.raises(ValueError):
+        entmax_attn_kv4(torch.zeros(2, 3, 1, 64, device="cuda"), cache, table, start)
+    with pytest.raises(ValueError):
+        entmax_attn_kv4(x.transpose(0, 1), cache, table, start)
