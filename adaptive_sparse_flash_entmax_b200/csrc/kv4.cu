@@ -767,7 +767,7 @@ __global__ void __launch_bounds__(kSolveThreads, 4) kv4_solve_kernel(const Kv4Ar
     int* js = solve_smem + kCap;                        // [kCap] their keys
     int* off = js + kCap;               // [nrun + 1] the runs' candidates before each run
     __shared__ float red[3][kSolveWarps];
-    __shared__ int box[kSolveWarps], box2[kSolveWarps];
+    __shared__ int box[kSolveWarps], box2[kSolveWarps], found;
     __shared__ float bc[2];
     __shared__ float halves[kSolveWarps][D];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -863,8 +863,9 @@ __global__ void __launch_bounds__(kSolveThreads, 4) kv4_solve_kernel(const Kv4Ar
 
     // ---- candidates above a bound of tau, in order, into shared memory.  All runs' entries are
     // one sequence, of which each warp takes an equal part.
-    // calls f(y, key, is there) for 32 of the entries [from, to) at a time
-    auto each = [&](int from, int to, auto f) {
+    // calls f(y, key, is there) for 32 of the entries [from, to) at a time, and after 128 of them
+    // stops where `enough` says so
+    auto each = [&](int from, int to, auto f, auto enough) {
         int i = 0;   // the run that holds the first entry (by halving), then forward
 #pragma unroll 1
         for (int step = kKvMaxRuns / 2; step > 0; step >>= 1)
@@ -884,6 +885,7 @@ __global__ void __launch_bounds__(kSolveThreads, 4) kv4_solve_kernel(const Kv4Ar
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) f(__int_as_float(c[u].x) - m, c[u].y, c[u].y >= 0);
+            if (enough()) break;
         }
     };
     auto part = [&](int n, int w) { return (int)((long long)n * w / kSolveWarps); };
@@ -912,11 +914,12 @@ __global__ void __launch_bounds__(kSolveThreads, 4) kv4_solve_kernel(const Kv4Ar
             if (i >= ends[k]) f = from[k + 1];
         return f + i;
     };
-    // the entries of the first n that lie above `bound`; false where they do not fit
+    // the entries of the first n that lie above `bound`; false where they are more than fit, which
+    // the warps' common count tells before all are looked through
     auto gather = [&](int n, float bound, int* total) {
         const int p0 = part(n, warp), p1 = part(n, warp + 1);
         auto place = [&](int room) {
-            mine = 0;
+            int told = mine = 0;
             each(p0, p1, [&](float y, int j, bool there) {
                 const bool take = there && y > bound;
                 const unsigned mask = __ballot_sync(kFull, take);
@@ -926,38 +929,57 @@ __global__ void __launch_bounds__(kSolveThreads, 4) kv4_solve_kernel(const Kv4Ar
                     js[e0 + p] = j;
                 }
                 mine += __popc(mask);
+            }, [&] {
+                if (lane == 0 && mine > told) atomicAdd(&found, mine - told);
+                told = mine;
+                return *const_cast<volatile int*>(&found) > kCap;
             });
         };
+        __syncthreads();
+        if (tid == 0) found = 0;
+        __syncthreads();
         // where all would fit, each warp has the room; else an equal share, and if that was too
         // little for one of them, what they counted
         const int room = n <= kCap ? p1 - p0 : kCap / kSolveWarps;
         e0 = n <= kCap ? p0 : warp * room;
         place(room);
-        if (__syncthreads_or(mine > room)) {
-            e0 = warps_before(mine, box, total);
-            if (*total > kCap) return false;
+        const bool again = __syncthreads_or(mine > room);
+        if (found > kCap) return false;
+        if (again) {
+            e0 = warps_before(mine, box, total);   // (its barriers: `found` was read by all)
+            if (tid == 0) found = 0;
+            __syncthreads();
             place(mine);
         }
         *total = close_up(mine);
         return true;
     };
-    // tau > m - 1.  Where there are far more entries than fit, tau also lies above the tau of
+    // tau > m - 1.  Where more entries lie above that than fit, tau also lies above the tau of
     // fewer keys: of the first runs that surely fit, then of eight times as many above that, and
-    // so on (with the dense weights of alpha 1.25 the first drops nine candidates of ten; without
-    // it a sequence of 100000 keys takes 710 us instead of 470, in passes over its lists; below
-    // 4 kCap entries most of which lie under m - 1, it costs 12 us of 108).
+    // so on (with the dense weights of alpha 1.25 the first drops nine candidates of ten).  What
+    // decides is the count above m - 1, which the keys alone determine; how many entries the lists
+    // hold besides is a matter of timing, and deciding by that number, though it spares a row of
+    // many entries the first look (sixteen sequences of 32768 at alpha 1.25 take 362 us, not 354;
+    // of 16384 with 4300 a row above m - 1 115, not 158), changed last bits from call to call.
     float bound = -1.f;
     int total = 0;
-    bool fits = true;
-    for (int runs = raw <= 4 * kCap ? nrun : max(1, kCap / stride);; runs = runs > nrun / 8 ? nrun : runs * 8) {
+    bool fits;
+    for (int runs = nrun, first = 1;; first = 0) {
         fits = gather(off[min(runs, nrun)], bound, &total);
+        if (first) {
+            if (fits) break;
+            runs = max(1, kCap / stride);
+            continue;
+        }
         if (runs >= nrun) break;
-        if (!fits || total == 0) continue;   // (no key of the first runs may be near m)
-        solve(total, -1.f, [&](auto add) {
-            for (int i = tid; i < total; i += kSolveThreads) add(ys[where(i)]);
-        });
-        bound = fmaxf(bound, sv.tau - 2e-6f);   // (it stops within 2e-7 of the sum, a step of it at most)
-        __syncthreads();
+        if (fits && total > 0) {   // (no key of the first runs may be near m)
+            solve(total, -1.f, [&](auto add) {
+                for (int i = tid; i < total; i += kSolveThreads) add(ys[where(i)]);
+            });
+            bound = fmaxf(bound, sv.tau - 2e-6f);   // (it stops within 2e-7 of the sum, a step of it at most)
+            __syncthreads();
+        }
+        runs = runs > nrun / 8 ? nrun : runs * 8;
     }
     if (!fits) {
         // scores too equal: the lists stay in the workspace, closed up so that what follows does

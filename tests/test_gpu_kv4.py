@@ -457,3 +457,32 @@ def test_wrapper_refusals_on_the_device():
         entmax_attn_kv4(torch.zeros(2, 3, 1, 64, device="cuda"), cache, table, start)
     with pytest.raises(ValueError):
         entmax_attn_kv4(x.transpose(0, 1), cache, table, start)
+
+
+@pytest.mark.parametrize("alpha,group,B", [(1.25, 8, 16), (1.5, 4, 32), (1.5, 1, 64), (2.0, 4, 32)])
+def test_attention_repeats_whatever_the_timing(alpha, group, B):
+    """Rows with 200 to 2000 keys above their maximum - 1, where how many more candidates the scores kernel
+    lists varies by hundreds from call to call: the same bits every time, with other work beside the calls."""
+    gen = torch.Generator().manual_seed(19)
+    n, d, page = 32768, 32, 128
+    cache = pool(n // page, 1, page, d, gen)
+    one = tables(1, n // page, n // page, gen).cuda()
+    k, _ = kv4_read(cache, one, i32([0]), n, dtype=torch.float32)
+    u = torch.randn(d, generator=gen).double().cuda()
+    x = (k[0, 0].double() @ u).sort(descending=True).values
+    # queries along u whose scores put key rank_r just at the maximum - 1
+    rank = torch.linspace(200, 2000, 4 * B * group).long()
+    beta = math.sqrt(d) / (alpha - 1) / (x[0] - x[rank.cuda()])
+    table, start = one.expand(B, -1).contiguous(), i32([n - 1] * B)
+    side, junk = torch.cuda.Stream(), torch.randn(1 << 20, device="cuda")
+    for part in beta.split(B * group):
+        q = (part[:, None] * u).float().view(B, group, 1, d).contiguous()
+        tau = torch.empty(B, group, 1, device="cuda")
+        o = entmax_attn_kv4(q, cache, table, start, alpha, tau=tau).clone()
+        first, differ = tau.clone(), torch.zeros((), dtype=torch.int64, device="cuda")
+        for i in range(60):   # (no wait between calls: it would even the timing out)
+            with torch.cuda.stream(side):
+                junk[:1 << (8 + i % 13)].sin_()
+            again = entmax_attn_kv4(q, cache, table, start, alpha, tau=tau)
+            differ += (again != o).sum() + (tau != first).sum()
+        assert int(differ) == 0
