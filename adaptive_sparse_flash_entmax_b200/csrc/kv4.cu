@@ -790,6 +790,8 @@ __global__ void __launch_bounds__(kSolveThreads, 4) kv4_solve_kernel(const Kv4Ar
     }
     auto list_of = [&](int i) { return cand + (size_t)i * stride; };
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    // (a call that covers no token has no scores kernel to report its lengths)
+    if (a.nchunk == 0 && s.bad && a.bad && hk == 0 && r == 0 && tid == 0) atomicOr(a.bad, s.bad);
 
     // ---- row maximum (every warp for itself), then the runs' offsets, a share each warp
     float m = -INFINITY;
@@ -1170,7 +1172,7 @@ cudaError_t attn(const Kv4Args& a, int gm, cudaStream_t s) {
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = a.nchunk > 0 ? 1 : 0;   // (behind a kernel that is not ours it starts in order: it reads the lengths first)
     auto kern = gm == 1 ? kv4_solve_kernel<T, D, 1> : gm == 2 ? kv4_solve_kernel<T, D, 2>
               : gm == 3 ? kv4_solve_kernel<T, D, 3> : gm == 4 ? kv4_solve_kernel<T, D, 4> : kv4_solve_kernel<T, D, 0>;
     return cudaLaunchKernelEx(&cfg, kern, a);

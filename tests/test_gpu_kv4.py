@@ -486,3 +486,17 @@ def test_attention_repeats_whatever_the_timing(alpha, group, B):
             again = entmax_attn_kv4(q, cache, table, start, alpha, tau=tau)
             differ += (again != o).sum() + (tau != first).sum()
         assert int(differ) == 0
+
+
+def test_no_cover_is_reported():
+    """max_len 0 or an empty table: a row that is there lies outside the cover, no row is fine."""
+    cache = kv4_alloc(1, 2, 16, 32, "cuda")
+    q = torch.randn(2, 4, 3, 32, device="cuda")
+    none = torch.empty((2, 0), dtype=torch.int32, device="cuda")
+    for start, lens, want in (([0, 0], [1, 0], 2), ([0, 0], [0, 3], 2), ([0, 0], [0, 0], 0), ([1, 0], [0, 0], 2),
+                              ([0, -1], [0, 0], 2), ([0, 0], None, 2)):
+        for table, kw in ((i32([[0], [0]]), dict(max_len=0)), (none, {})):
+            bad = i32([0])
+            o = entmax_attn_kv4(q, cache, table, i32(start), 1.5, new_lens=None if lens is None else i32(lens),
+                                bad=bad, **kw)
+            assert int(bad) == want and not bool(o.any())
