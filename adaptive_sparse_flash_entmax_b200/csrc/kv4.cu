@@ -679,11 +679,11 @@ __global__ void __launch_bounds__(kScoreThreads, R == 4 ? 4 : R == 8 ? 3 : 2) kv
         for (int o = 1; o < LPR; o <<= 1) m = max_nan(m, __shfl_xor_sync(kFull, m, o));
         if (sub == 0) *const_cast<volatile float*>(&row_max[lrow]) = m;
         // above m - 1, and the maximum itself: where |m| >= 2^24 makes them equal, the limit is
-        // the next float below m (m = -inf or NaN: it is NaN, and nothing is above).  (A higher
-        // bound of tau, proved by the run's own keys, halves the candidates of a run of 20 chunks
-        // and costs as much as they do.)
+        // the next float below m (m = -inf: the step gives NaN; m = NaN: m - 1 is; nothing is above
+        // either).  (A higher bound of tau, proved by the run's own keys, halves the candidates of a
+        // run of 20 chunks and costs as much as they do.)
         float lim = m - 1.f;
-        if (!(lim < m)) lim = __int_as_float(__float_as_int(m) + (m > 0.f ? -1 : 1));
+        if (lim >= m) lim = __int_as_float(__float_as_int(m) + (m > 0.f ? -1 : 1));
         unsigned take = 0;
 #pragma unroll
         for (int k = 0; k < KPL; ++k) take |= (v[k] > lim ? 1u : 0u) << k;

@@ -500,3 +500,16 @@ def test_no_cover_is_reported():
             o = entmax_attn_kv4(q, cache, table, i32(start), 1.5, new_lens=None if lens is None else i32(lens),
                                 bad=bad, **kw)
             assert int(bad) == want and not bool(o.any())
+
+
+def test_a_row_of_nan_lists_no_keys():
+    """Of a row that has met a NaN the call keeps its runs' maxima and counts, no candidates: of 64 keys (one run)
+    two words a row are written to the workspace."""
+    gen = torch.Generator().manual_seed(20)
+    cache = pool(4, 1, 16, 32, gen)
+    cache[1][0, 0, 3] = math.nan
+    table, q = i32([[0, 1, 2, 3]]), torch.randn(1, 8, 1, 32, generator=gen).cuda()
+    ws = kv4_workspace(q, cache, table).fill_(0x5A)
+    o = entmax_attn_kv4(q, cache, table, i32([63]), 1.5, ws=ws)
+    assert bool(torch.isnan(o).all())
+    assert int((ws.view(torch.int32) != 0x5A5A5A5A).sum()) <= 2 * 8
