@@ -272,12 +272,19 @@ __global__ void __launch_bounds__(kKvThreads) kv4_read_kernel(const Kv4Args a) {
 // the second sum as a product too: a lane's pair of group c is two elements of an A operand,
 // met by (0, sum q of group c) in three bf16 parts (24 bits).
 // The queries are fp16, scaled per row by a power of two so that the largest lies in
-// [2^14, 2^15): exact for bf16 values down to 2^-31 of the largest, below which the
-// rounding is 2^-39 of it; a float32 row is the sum of two such halves (22 bits).  Float32
-// scores are then off by what the product truncates, about 2^-24 of its largest term for each
-// of 16: O is at 2e-6 to 3e-6 of the 64-bit result where a plain float form has 0.5e-6 to
-// 0.9e-6 (codes less 8, a float zeros' term and rounded joins of the partial products were
-// tried and bring nothing).
+// [2^14, 2^15): exact for bf16 values down to 2^-27 of the largest (2^-31 in the dimensions
+// without the 1/16), below which the rounding is 2^-35 (2^-39) of it.  The products' sums lose
+// what lies under 2^-24 of their largest term, and the pair's terms largely cancel (codes lie
+// about 8, zero about -8 scale): bf16 results do not see it, float32 ones would.
+// A float32 row is hi + mid: hi a multiple of 16, so that every partial sum of codes . hi is a
+// multiple of 16 below 2^24 and the product exact, mid the rest rounded to fp16 (2^-23 of the
+// row's largest value at most).  The sums begin at -8 sum hi, which centres the codes, and are
+// joined in float:
+//     q.k = sum_groups scale * (((codes - 8) . hi) + codes . mid) + (zero + 8 scale) sum hi + zero sum mid.
+// O then lies 0.3e-6 to 0.6e-6 from the 64-bit result, where plain float products of the same keys
+// leave 0.4e-6 to 1.6e-6; with one chain of truncated sums, queries of two times 11 bits and the
+// zeros' term as a product it was 1.2e-6 to 2.9e-6, and calls were 2 to 7 % shorter (16 x 8192 of
+// 32 heads of 128: 50 us instead of 51; eight rows of 4 x 8192: 79 instead of 85).
 // The scores of a chunk pass through the warp's shared memory (queries by keys), where 32/R
 // lanes a row take their maximum and the candidates above the CTA's maximum so far - 1 (which
 // of the warps got how far does not matter: the solver drops what the final maximum rules out).
@@ -451,8 +458,9 @@ __global__ void __launch_bounds__(kScoreThreads, R == 4 ? 4 : R == 8 ? 3 : 2) kv
     // ---- queries: lane (n = lane / 4, c = lane % 4) holds dimensions 32 w + 8 c + i of row n
     // (PAIR: row n % 4, and of its two groups the one that columns 0-3 or 4-7 take)
     constexpr int QG = PAIR ? GS : G;
-    uint32_t qf[NT][QG][4], ql[F32 ? NT : 1][QG][4];   // B operands; float32 rows: high and low parts
-    uint32_t qz[NT][3];                              // sum q of group c in three parts
+    uint32_t qf[NT][QG][4], ql[F32 ? NT : 1][QG][4];   // B operands; float32 rows: hi and mid
+    uint32_t qz[F32 ? 1 : NT][3];                    // sum q of group c in three parts
+    float sh[F32 ? NT : 1][QG][2], sm[F32 ? NT : 1][QG][2];   // float32: sum hi, sum mid of columns 2c, 2c + 1
     uint32_t qb[PAIR ? QG : 1][4][2], qbl[PAIR && F32 ? QG : 1][4][2];   // PAIR: the two halves of the operand
     float mul = 0.f, mul2 = 1.f;                     // of row lrow: x = mul mul2 acc
 #pragma unroll
@@ -499,11 +507,24 @@ __global__ void __launch_bounds__(kScoreThreads, R == 4 ? 4 : R == 8 ? 3 : 2) kv
 #pragma unroll
             for (int k = 0; k < 8; ++k) y[k] = PAIR && key >= 4 ? x[(g + GS) % G][k] : x[g][k];
             if constexpr (F32) {
+                float hs = 0.f, ms = 0.f;
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
-                    const float hi = __half2float(__float2half_rn(y[k]));
+                    const float hi = rintf(y[k] * 0.0625f) * 16.f;
                     lo[k] = y[k] - hi;
                     y[k] = hi;
+                    hs += hi;
+                    ms += lo[k];
+                }
+#pragma unroll
+                for (int o = 1; o < 4; o <<= 1) {
+                    hs += __shfl_xor_sync(kFull, hs, o);
+                    ms += __shfl_xor_sync(kFull, ms, o);
+                }
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    sh[nt][g][k] = __shfl_sync(kFull, hs, 4 * (2 * c + k)) * 5.9604644775390625e-08f;
+                    sm[nt][g][k] = __shfl_sync(kFull, ms, 4 * (2 * c + k)) * 5.9604644775390625e-08f;
                 }
             }
             const float f = 0.0625f;
@@ -518,8 +539,10 @@ __global__ void __launch_bounds__(kScoreThreads, R == 4 ? 4 : R == 8 ? 3 : 2) kv
                 ql[nt][g][3] = pack_half(lo[3] * f, lo[7] * f);
             }
         }
+        if constexpr (!F32) {
 #pragma unroll
-        for (int t = 0; t < 3; ++t) qz[nt][t] = bf16_part(zsum);
+            for (int t = 0; t < 3; ++t) qz[nt][t] = bf16_part(zsum);
+        }
         // x = cx 2^(24 - e) s, in two factors where one would overflow (24 - e <= 137);
         // a row with a NaN or an infinity has NaN scores
         const int e1 = min(24 - e, 100);
@@ -573,21 +596,26 @@ __global__ void __launch_bounds__(kScoreThreads, R == 4 ? 4 : R == 8 ? 3 : 2) kv
                 load_words<GS>(lane_meta + stage * L::kStage + (u * kKvTile + 8 * h) * kMetaB, mt[h]);
             }
             float acc[NT][4];
-            uint32_t mz[2];   // the pair of group c (PAIR with two groups: of group c/2; else zeros)
+            if constexpr (F32) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if constexpr (PAIR && G == 4) mz[h] = c & 1 ? mt[h][GS - 1] : mt[h][0];
-                else if constexpr (PAIR) mz[h] = c & 1 ? 0u : mt[h][0];
-                else {
-                    mz[h] = c == 0 ? mt[h][0] : 0u;
+                for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
+            } else {
+                uint32_t mz[2];   // the pair of group c (PAIR with two groups: of group c/2; else zeros)
 #pragma unroll
-                    for (int g = 1; g < G; ++g) mz[h] = c == g ? mt[h][g] : mz[h];
+                for (int h = 0; h < 2; ++h) {
+                    if constexpr (PAIR && G == 4) mz[h] = c & 1 ? mt[h][GS - 1] : mt[h][0];
+                    else if constexpr (PAIR) mz[h] = c & 1 ? 0u : mt[h][0];
+                    else {
+                        mz[h] = c == 0 ? mt[h][0] : 0u;
+#pragma unroll
+                        for (int g = 1; g < G; ++g) mz[h] = c == g ? mt[h][g] : mz[h];
+                    }
                 }
-            }
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                mma_16816_bf_0(acc[nt], mz[0], mz[1], mz[0], mz[1], qz[nt][0], qz[nt][1]);
-                mma_1688_bf(acc[nt], mz[0], mz[1], qz[nt][2]);
+                for (int nt = 0; nt < NT; ++nt) {
+                    mma_16816_bf_0(acc[nt], mz[0], mz[1], mz[0], mz[1], qz[nt][0], qz[nt][1]);
+                    mma_1688_bf(acc[nt], mz[0], mz[1], qz[nt][2]);
+                }
             }
             // a word's codes as four pairs of halves
             auto halves = [](uint32_t x, uint32_t (&h)[4]) {
@@ -599,39 +627,67 @@ __global__ void __launch_bounds__(kScoreThreads, R == 4 ? 4 : R == 8 ? 3 : 2) kv
             };
 #pragma unroll
             for (int g = 0; g < GS; ++g) {
-                const float s0 = bf16_lo(mt[0][g]), s1 = bf16_lo(mt[1][g]);
+                const float sc[2] = {bf16_lo(mt[0][g]), bf16_lo(mt[1][g])};
                 uint32_t k0h[4], k1h[4];
                 halves(w[0][g], k0h);
                 halves(w[1][g], k1h);
+                // float32: acc of keys h, columns k from its two sums
+                auto join = [&](float (&r)[4], int nt, const float (&dh)[4], const float (&dm)[4]) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float z = bf16_hi(mt[h][g]), zc = fmaf(8.f, sc[h], z);
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            float t = fmaf(z, sm[nt][g][k], r[2 * h + k]);
+                            t = fmaf(zc, sh[nt][g][k], t);
+                            r[2 * h + k] = fmaf(sc[h], dh[2 * h + k] + dm[2 * h + k], t);
+                        }
+                    }
+                };
                 if constexpr (PAIR) {
                     uint32_t o0[4], o1[4];   // the second group's
                     halves(w[0][g + GS], o0);
                     halves(w[1][g + GS], o1);
                     float d[4];
+                    if constexpr (F32) {
+                        float dm[4];
 #pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-                        if (t == 0) mma_16816_0(d, k0h[t], k1h[t], o0[t], o1[t], qb[g][t][0], qb[g][t][1]);
-                        else mma_16816(d, k0h[t], k1h[t], o0[t], o1[t], qb[g][t][0], qb[g][t][1]);
-                        if constexpr (F32) mma_16816(d, k0h[t], k1h[t], o0[t], o1[t], qbl[g][t][0], qbl[g][t][1]);
+                        for (int k = 0; k < 4; ++k) d[k] = -8.f * sh[0][g][k & 1];
+#pragma unroll
+                        for (int t = 0; t < 4; ++t) {
+                            mma_16816(d, k0h[t], k1h[t], o0[t], o1[t], qb[g][t][0], qb[g][t][1]);
+                            if (t == 0) mma_16816_0(dm, k0h[t], k1h[t], o0[t], o1[t], qbl[g][t][0], qbl[g][t][1]);
+                            else mma_16816(dm, k0h[t], k1h[t], o0[t], o1[t], qbl[g][t][0], qbl[g][t][1]);
+                        }
+                        join(acc[0], 0, d, dm);
+                    } else {
+#pragma unroll
+                        for (int t = 0; t < 4; ++t) {
+                            if (t == 0) mma_16816_0(d, k0h[t], k1h[t], o0[t], o1[t], qb[g][t][0], qb[g][t][1]);
+                            else mma_16816(d, k0h[t], k1h[t], o0[t], o1[t], qb[g][t][0], qb[g][t][1]);
+                        }
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) acc[0][k] = fmaf(sc[k >> 1], d[k], acc[0][k]);
                     }
-                    acc[0][0] = fmaf(s0, d[0], acc[0][0]);
-                    acc[0][1] = fmaf(s0, d[1], acc[0][1]);
-                    acc[0][2] = fmaf(s1, d[2], acc[0][2]);
-                    acc[0][3] = fmaf(s1, d[3], acc[0][3]);
                 } else {
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         float d[4];
-                        mma_16816_0(d, k0h[0], k1h[0], k0h[1], k1h[1], qf[nt][g][0], qf[nt][g][1]);
-                        mma_16816(d, k0h[2], k1h[2], k0h[3], k1h[3], qf[nt][g][2], qf[nt][g][3]);
                         if constexpr (F32) {
-                            mma_16816(d, k0h[0], k1h[0], k0h[1], k1h[1], ql[nt][g][0], ql[nt][g][1]);
-                            mma_16816(d, k0h[2], k1h[2], k0h[3], k1h[3], ql[nt][g][2], ql[nt][g][3]);
+                            float dm[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) d[k] = -8.f * sh[nt][g][k & 1];
+                            mma_16816(d, k0h[0], k1h[0], k0h[1], k1h[1], qf[nt][g][0], qf[nt][g][1]);
+                            mma_16816(d, k0h[2], k1h[2], k0h[3], k1h[3], qf[nt][g][2], qf[nt][g][3]);
+                            mma_16816_0(dm, k0h[0], k1h[0], k0h[1], k1h[1], ql[nt][g][0], ql[nt][g][1]);
+                            mma_16816(dm, k0h[2], k1h[2], k0h[3], k1h[3], ql[nt][g][2], ql[nt][g][3]);
+                            join(acc[nt], nt, d, dm);
+                        } else {
+                            mma_16816_0(d, k0h[0], k1h[0], k0h[1], k1h[1], qf[nt][g][0], qf[nt][g][1]);
+                            mma_16816(d, k0h[2], k1h[2], k0h[3], k1h[3], qf[nt][g][2], qf[nt][g][3]);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) acc[nt][k] = fmaf(sc[k >> 1], d[k], acc[nt][k]);
                         }
-                        acc[nt][0] = fmaf(s0, d[0], acc[nt][0]);
-                        acc[nt][1] = fmaf(s0, d[1], acc[nt][1]);
-                        acc[nt][2] = fmaf(s1, d[2], acc[nt][2]);
-                        acc[nt][3] = fmaf(s1, d[3], acc[nt][3]);
                     }
                 }
             }
@@ -1160,7 +1216,9 @@ cudaError_t attn(const Kv4Args& a, int gm, cudaStream_t s) {
         case 4: e = launch_scores<T, D, 4>(a, s); break;
         case 8: e = launch_scores<T, D, 8>(a, s); break;
         case 16: e = launch_scores<T, D, 16>(a, s); break;
-        default: e = launch_scores<T, D, 32>(a, s); break;
+        default:   // (float32 rows of 128 stay at 16)
+            if constexpr (!(sizeof(T) == 4 && D == 128)) e = launch_scores<T, D, 32>(a, s);
+            break;
     }
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};

@@ -513,3 +513,37 @@ def test_a_row_of_nan_lists_no_keys():
     o = entmax_attn_kv4(q, cache, table, i32([63]), 1.5, ws=ws)
     assert bool(torch.isnan(o).all())
     assert int((ws.view(torch.int32) != 0x5A5A5A5A).sum()) <= 2 * 8
+
+
+@pytest.mark.parametrize("d,n,Hq,L,alpha,beta", [(128, 2048, 4, 1, 1.5, 1.0), (128, 1500, 4, 4, 1.5, 2.0),
+                                                 (64, 3000, 4, 5, 2.0, 1.0), (64, 1000, 1, 1, 1.5, 1.0),
+                                                 (32, 1500, 4, 2, 1.25, 1.0), (32, 900, 2, 6, 1.5, 4.0)])
+def test_float32_is_as_near_as_float_products(d, n, Hq, L, alpha, beta):
+    """float32 rows: the error (2-norm) is no more than that of the exact entmax of float32 scores.  Those come from
+    sums of d terms, each rounded; the kernel's sums over a group of 32 are exact in the query's leading 11 bits and
+    it rounds four times a group (2^-24 of the partial sum each), a query's value to 2^-23 of its row's largest.
+    Beside the scores: |sum p - 1| <= 2e-7 where the solver stops and 2^-24 for each of p and o: 3e-7."""
+    gen = torch.Generator().manual_seed(21)
+    page, B = 16, 8
+    used = -(-n // page)
+    cache = pool(used, 1, page, d, gen)
+    one = tables(1, used, used, gen).cuda()
+    q = (beta * torch.randn(B, Hq, L, d, generator=gen)).cuda()
+    o = entmax_attn_kv4(q, cache, one.expand(B, -1).contiguous(), i32([n - L] * B), alpha)
+    k, v = (t[0, 0] for t in kv4_read(cache, one, i32([0]), n, dtype=torch.float32))
+    seen = torch.arange(n, device="cuda")[None] <= (n - L + torch.arange(L, device="cuda"))[:, None]
+
+    def exact(x):   # of the given scores, by halving
+        x = x.double().masked_fill(~seen, -math.inf)
+        hi = x.amax(-1, keepdim=True)
+        lo = hi - 1
+        for _ in range(56):
+            mid = (lo + hi) / 2
+            up = torch.relu(x - mid).pow(1 / (alpha - 1)).sum(-1, keepdim=True) > 1
+            lo, hi = torch.where(up, mid, lo), torch.where(up, hi, mid)
+        return torch.relu(x - (lo + hi) / 2).pow(1 / (alpha - 1)) @ v.double()
+
+    assert not torch.backends.cuda.matmul.allow_tf32
+    want = exact(q.double() @ k.double().T * ((alpha - 1) / math.sqrt(d)))
+    plain = exact(q @ k.T * ((alpha - 1) / math.sqrt(d)))
+    assert float((o.double() - want).norm()) <= float((plain - want).norm()) + 3e-7 * float(want.norm())
