@@ -701,21 +701,28 @@ extern "C" ent_status ent_attn_noalloc_read_status(long long* counters, void* st
 // ---------------------------------------------------------------- 4-bit cache
 namespace {
 
-// Pool, block table and row counts of a call; fills a.g, a.Hkv, a.table, a.start, a.new_lens.
-ent_status check_kv4(ent::Kv4Args& a, const void* kc, const void* km, const void* vc, const void* vm,
-                     int pages, int page, const int32_t* table, int max_pages, const int32_t* start,
-                     const int32_t* new_lens, int B, int Hkv, int L, int d, int dtype, int32_t* bad) {
+// Sizes of a call; `cover` the tokens its block table names or its max_len bounds.
+ent_status check_kv4_sizes(int B, int Hkv, int L, int d, int dtype, long long cover) {
     if (B < 0 || Hkv < 1 || L < 0) return fail(ENT_EINVAL, "bad size (B=%d Hkv=%d L=%d)", B, Hkv, L);
     if (dtype != ENT_F32 && dtype != ENT_BF16) return fail(ENT_EINVAL, "unknown dtype %d", dtype);
     if (d != 32 && d != 64 && d != 128)
         return fail(ENT_EUNSUPPORTED, "head dim d=%d (supported: 32, 64, 128)", d);
+    if ((long long)B * Hkv > 65535) return fail(ENT_EUNSUPPORTED, "B*Hkv=%lld exceeds 65535", (long long)B * Hkv);
+    if (cover > 1ll << 30)   // positions and chunk ends stay clear of 31 bits
+        return fail(ENT_EUNSUPPORTED, "%lld tokens a sequence exceed 2^30", cover);
+    if ((long long)B * Hkv * L > 0x7fffffffll) return fail(ENT_EUNSUPPORTED, "B*Hkv*L exceeds 31 bits");
+    return ENT_OK;
+}
+
+// Pool, block table and row counts of a call; fills a.g, a.Hkv, a.table, a.start, a.new_lens.
+ent_status check_kv4(ent::Kv4Args& a, const void* kc, const void* km, const void* vc, const void* vm,
+                     int pages, int page, const int32_t* table, int max_pages, const int32_t* start,
+                     const int32_t* new_lens, int B, int Hkv, int L, int d, int dtype, int32_t* bad) {
     if (page < ent::kKvTile || (page & (page - 1)) != 0)
         return fail(ENT_EINVAL, "page of %d tokens (a power of two of at least %d)", page, ent::kKvTile);
     if (max_pages < 0) return fail(ENT_EINVAL, "negative size (max_pages=%d)", max_pages);
-    if ((long long)B * Hkv > 65535) return fail(ENT_EUNSUPPORTED, "B*Hkv=%lld exceeds 65535", (long long)B * Hkv);
-    if ((long long)max_pages * page > 1ll << 30)   // positions and chunk ends stay clear of 31 bits
-        return fail(ENT_EUNSUPPORTED, "max_pages * page = %lld tokens exceed 2^30", (long long)max_pages * page);
-    if ((long long)B * Hkv * L > 0x7fffffffll) return fail(ENT_EUNSUPPORTED, "B*Hkv*L exceeds 31 bits");
+    const ent_status st = check_kv4_sizes(B, Hkv, L, d, dtype, (long long)max_pages * page);
+    if (st != ENT_OK) return st;
     if (B > 0 && L > 0) {
         if ((!table && max_pages > 0) || !start) return fail(ENT_EINVAL, "null block_table/start pointer");
         if (pages < 1) return fail(ENT_EINVAL, "a pool without pages");
@@ -766,19 +773,19 @@ bool kv4_layout(const ent::Kv4Geom& g, long long rows, int group, int d, int dty
     return true;
 }
 
-ent_status check_kv4_attn(ent::Kv4Args& a, int Hq, int max_len, int window, int sinks, int d, int dtype,
+// Sizes of the attention alone; also its workspace's layout.
+ent_status check_kv4_attn(ent::Kv4Geom& g, int Hq, int Hkv, int max_len, int window, int sinks, int d, int dtype,
                           Kv4Layout* l) {
-    if (Hq < 1 || Hq % a.Hkv != 0) return fail(ENT_EINVAL, "Hq=%d is no multiple of Hkv=%d", Hq, a.Hkv);
+    if (Hq < 1 || Hq % Hkv != 0) return fail(ENT_EINVAL, "Hq=%d is no multiple of Hkv=%d", Hq, Hkv);
     if (window < 0 || sinks < 0) return fail(ENT_EINVAL, "negative window=%d or sinks=%d", window, sinks);
     if (sinks > 0 && window == 0) return fail(ENT_EINVAL, "sinks=%d without a window", sinks);
     if (max_len < 0) return fail(ENT_EINVAL, "negative max_len=%d", max_len);
-    a.group = Hq / a.Hkv;
-    a.g.max_len = max_len;
-    a.g.window = window;
-    a.g.sinks = sinks;
-    if (!kv4_layout(a.g, (long long)a.g.B * Hq * a.g.L, a.group, d, dtype, l))
+    g.max_len = max_len;
+    g.window = window;
+    g.sinks = sinks;
+    if (!kv4_layout(g, (long long)g.B * Hq * g.L, Hq / Hkv, d, dtype, l))
         return fail(ENT_EUNSUPPORTED, "B*Hq*L=%lld rows, %lld of one key head, are too many",
-                    (long long)a.g.B * Hq * a.g.L, (long long)a.g.L * a.group);
+                    (long long)g.B * Hq * g.L, (long long)g.L * (Hq / Hkv));
     return ENT_OK;
 }
 
@@ -821,13 +828,12 @@ ent_status ent_attn_kv4_read(const void* k_codes, const void* k_meta, const void
 
 size_t ent_attn_kv4_workspace_size(int B, int Hq, int Hkv, int L, int d, int dtype, int max_len,
                                    int window, int sinks) {
-    if (B < 0 || Hkv < 1 || Hq < 1 || Hq % Hkv != 0 || L < 0 || max_len < 0 || window < 0 || sinks < 0 ||
-        (sinks > 0 && window == 0))
-        return 0;
     ent::Kv4Geom g{};
-    g.B = B; g.L = L; g.max_len = max_len; g.window = window; g.sinks = sinks;
+    g.B = B; g.L = L;
     Kv4Layout l;
-    return kv4_layout(g, (long long)B * Hq * L, Hq / Hkv, d, dtype, &l) ? l.total : 0;
+    const bool fine = check_kv4_sizes(B, Hkv, L, d, dtype, max_len) == ENT_OK &&
+                      check_kv4_attn(g, Hq, Hkv, max_len, window, sinks, d, dtype, &l) == ENT_OK;
+    return fine ? l.total : 0;
 }
 
 ent_status ent_attn_kv4_fwd(const void* q, int B, int Hq, int Hkv, int L, int d, int dtype,
@@ -844,7 +850,8 @@ ent_status ent_attn_kv4_fwd(const void* q, int B, int Hq, int Hkv, int L, int d,
     if (max_len > a.g.max_len)
         return fail(ENT_EINVAL, "max_len=%d exceeds max_pages * page = %d", max_len, a.g.max_len);
     Kv4Layout l;
-    if ((st = check_kv4_attn(a, Hq, max_len, window, sinks, d, dtype, &l)) != ENT_OK) return st;
+    if ((st = check_kv4_attn(a.g, Hq, Hkv, max_len, window, sinks, d, dtype, &l)) != ENT_OK) return st;
+    a.group = Hq / Hkv;
     if (B == 0 || L == 0) return ENT_OK;
     if (!q || !o) return fail(ENT_EINVAL, "null q/o pointer");
     if (!aligned16(q) || !aligned16(o)) return fail(ENT_EINVAL, "q/o must be 16-byte aligned");

@@ -157,3 +157,19 @@ def test_restated_quantiser_bounds():
     # constant groups are held to bf16 rounding
     codes, scale, zero = kv4_ref.quantise(torch.full((1, 32), 1.7))
     assert float(zero) == float(torch.tensor(1.7).bfloat16()) and int(codes.max()) <= 15
+
+
+def test_no_workspace_for_what_the_call_refuses(lib):
+    """The size is 0 for every size that the call itself refuses, the limits among them."""
+    ok = dict(B=2, Hq=4, Hkv=2, L=3, d=64, dtype=capi.ENT_BF16, max_len=64, window=0, sinks=0)
+    assert capi.ent_attn_kv4_workspace_size(**ok) > 0
+    for kw in (dict(d=96), dict(d=0), dict(dtype=5), dict(B=70000), dict(max_len=(1 << 30) + 1), dict(L=1 << 30),
+               dict(B=-1), dict(Hkv=0), dict(Hq=0), dict(Hq=3), dict(L=-1), dict(max_len=-1), dict(window=-1),
+               dict(sinks=-1, window=4), dict(sinks=1)):
+        args = dict(ok, **kw)
+        assert capi.ent_attn_kv4_workspace_size(**args) == 0, kw
+        covered = max(args.pop("max_len"), 0)
+        st = capi.ent_attn_kv4_fwd(q=FAKE, o=FAKE, tau=None, alpha=1.5, **POOL, block_table=FAKE, start=FAKE,
+                                   max_pages=-(-covered // POOL["page"]), new_lens=None, bad=None,
+                                   max_len=dict(ok, **kw)["max_len"], ws=FAKE, ws_bytes=0, stream=None, **args)
+        assert st in (capi.ENT_EINVAL, capi.ENT_EUNSUPPORTED), kw
