@@ -236,9 +236,9 @@ def ent_attn_kv4_workspace_size(B, Hq, Hkv, L, d, dtype, max_len, window, sinks)
     return load().ent_attn_kv4_workspace_size(B, Hq, Hkv, L, d, dtype, max_len, window, sinks)
 
 
-def ent_attn_kv4_fwd(q, B, Hq, Hkv, L, d, dtype, float(alpha), window, sinks, k_codes, k_meta, v_codes,
+def ent_attn_kv4_fwd(q, B, Hq, Hkv, L, d, dtype, alpha, window, sinks, k_codes, k_meta, v_codes,
                      v_meta, pages, page, block_table, max_pages, start, new_lens, max_len, o, tau,
                      bad, ws, ws_bytes, stream) -> int:
-    return load().ent_attn_kv4_fwd(q, B, Hq, Hkv, L, d, dtype, float(alpha), window, sinks, k_codes,
+    return load().ent_attn_kv4_fwd(q, B, Hq, Hkv, L, d, dtype, alpha, window, sinks, k_codes,
                                    k_meta, v_codes, v_meta, pages, page, block_table, max_pages,
                                    start, new_lens, max_len, o, tau, bad, ws, ws_bytes, stream)

@@ -4,7 +4,6 @@ import os
 import shutil
 import subprocess
 
-import numpy as np
 import pytest
 import torch
 
@@ -174,12 +173,3 @@ def test_no_workspace_for_what_the_call_refuses(lib):
                                    max_pages=-(-covered // POOL["page"]), new_lens=None, bad=None,
                                    max_len=dict(ok, **kw)["max_len"], ws=FAKE, ws_bytes=0, stream=None, **args)
         assert st in (capi.ENT_EINVAL, capi.ENT_EUNSUPPORTED), kw
-
-
-@pytest.mark.parametrize("alpha", [np.float32(2.5), torch.tensor(2.5)])
-def test_alpha_of_any_number_type(lib, alpha):
-    """As the other calls take it: a number that is no Python float is converted (here to one that is refused)."""
-    args = dict(POOL, **SEQ, **ROWS, Hq=4, q=FAKE, o=FAKE, tau=None, window=0, sinks=0, max_len=64, ws=FAKE,
-                ws_bytes=1 << 30)
-    assert capi.ent_attn_kv4_fwd(**args, alpha=alpha) == capi.ENT_EINVAL
-    assert "alpha" in capi.ent_attn_last_error()
