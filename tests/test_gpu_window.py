@@ -217,3 +217,20 @@ def test_long_window():
         want = p @ vv
         tol = 2.0 ** -8 * (p @ vv.abs()) + 1e-4 * vv.abs().max() + 1e-5
         assert bool(((o[i].double() - want).abs() <= tol + 2.0 ** -8 * (want.abs() + tol)).all())
+
+
+@pytest.mark.parametrize("alpha,beta", [(1.5, 1.0), (1.5, 4.0)])
+def test_a_bfloat16_window_over_everything_has_all_that_causal_attention_has(alpha, beta):
+    """Over 64 tiles, where the bound pass skips blocks and the start is calibrated: the same bits and the same work,
+    forward and backward; one key less is a window."""
+    N = 8400
+    q, k, v, do = make(1, 1, N, 64, "bf16", 11, beta)
+    ws = A.workspace(1 << 26, q.device)
+    runs = []
+    for kw in ({}, dict(window=N, sinks=3), dict(window=10 ** 12), dict(window=N - 1)):
+        o, tau, mask, _ = A.entmax_attn_fwd(q, k, v, alpha, True, ws=ws, **kw)
+        work = A.read_status(ws)
+        runs.append((work[0], o, tau, mask, *A.entmax_attn_bwd(q, k, v, o, do, tau, mask, alpha, True, **kw)))
+    for other in runs[1:3]:
+        assert other[0] == runs[0][0] and all(torch.equal(a, b) for a, b in zip(other[1:], runs[0][1:]))
+    assert runs[3][0] != runs[0][0]
