@@ -203,7 +203,8 @@ __global__ void __launch_bounds__(kWinThreads) win_fwd_f32_kernel(const FwdArgs 
     }
     if (i < N) {
         store_row<D>(static_cast<float*>(a.o) + head + (size_t)i * D + c0, acc, 1.f);
-        if (a.otilde) store_row<D>(a.otilde + head + (size_t)i * D + c0, accg, 1.f / gsum[row]);
+        if (a.otilde)   // (no weight at all, as of a query with a NaN: zeros)
+            store_row<D>(a.otilde + head + (size_t)i * D + c0, accg, gsum[row] > 0.f ? 1.f / gsum[row] : 0.f);
     }
     if (tid == 0 && i0 % kBlk == 0) {   // counted once per 128-row tile, whose scores are computed once
         const WinBlocks wb(a.window, a.sinks, i0 / kBlk);

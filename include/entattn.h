@@ -225,6 +225,11 @@ ent_status ent_attn_bwd_lists(const void *q, const void *k, const void *v,
  * bracket's midpoint.  otilde (nullable) as in ent_attn_fwd_otilde / ent_attn_bwd_otilde:
  * the forward fills it, the backward then takes delta from it; with NULL the backward
  * recomputes delta.  The backward's window and sinks must be the forward's.
+ * What is no number: here and in ent_attn_fwd a query with a NaN or an infinity has no score to
+ * weigh; its row of O is zeros, its tau not finite, and its row of dQ zeros (the attention over
+ * the cache, below, gives NaN for it).  What else a NaN or an infinity does is confined to blocks:
+ * one in k or v to the rows of O and dQ of the 128-row tiles that see its key block, one in q or
+ * dO to the rows of dK and dV in the key blocks that its tile sees; what those hold is unspecified.
  */
 ent_status ent_attn_fwd_window(const void *q, const void *k, const void *v,
                                int B, int H, int N, int d, int dtype, float alpha,

@@ -234,3 +234,29 @@ def test_a_bfloat16_window_over_everything_has_all_that_causal_attention_has(alp
     for other in runs[1:3]:
         assert other[0] == runs[0][0] and all(torch.equal(a, b) for a, b in zip(other[1:], runs[0][1:]))
     assert runs[3][0] != runs[0][0]
+
+
+@pytest.mark.parametrize("kw", [{}, dict(window=64, sinks=2), dict(window=1700, sinks=3)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_a_query_that_is_no_number(bad, dtype, kw):
+    """It has no weights: zeros in O and dQ, tau not finite, by every kernel and with either delta; the other rows'
+    O and dQ keep their bits."""
+    N, r = 1750, 900
+    q, k, v, do = make(1, 2, N, 64, dtype, 12)
+    ot = torch.empty(q.shape, device="cuda")
+
+    def both(q):
+        o, tau, mask, _ = A.entmax_attn_fwd(q, k, v, 1.5, True, otilde=ot, **kw)
+        dq = A.entmax_attn_bwd(q, k, v, None, do, tau, mask, 1.5, True, otilde=ot, **kw)[0]
+        return o, dq, A.entmax_attn_bwd(q, k, v, o, do, tau, mask, 1.5, True, **kw)[0], tau
+
+    clean = both(q)
+    spoilt = q.clone()
+    spoilt[0, 1, r, 7] = bad
+    got = both(spoilt)
+    assert not bool(torch.isfinite(got[3][0, 1, r]))
+    for a, b in zip(got[:3], clean[:3]):
+        assert not bool(a[0, 1, r].any())      # (a NaN is true)
+        a[0, 1, r] = b[0, 1, r]
+        assert torch.equal(a, b)
