@@ -1,5 +1,6 @@
 // win_f32.cu -- float32 attention under a sliding window, forward and backward, where the
-// visible scores of 16 query rows fit in shared memory (window + sinks up to about 1500).
+// visible scores of 16 query rows fit in shared memory (window + sinks up to 1584 at d = 32,
+// 1392 at 64, 1072 at 128).
 //
 //     s = Q K^T / sqrt(d),  x = (alpha-1) s,  u = (x - tau)_+,  p = u^gamma,  sum p = 1,  O = P V,
 //     g = u^(gamma-1),  delta = sum g dP / sum g,  dS = g (dP - delta),  dP = dO V^T,
@@ -412,7 +413,11 @@ cudaError_t win_bwd_d(const BwdArgs& a, int gm, cudaStream_t s) {
 }  // namespace
 
 // The backward's two score arrays are the larger need: both directions take this path, or
-// neither (they share tau to the last bit of the scores).
+// neither (they share tau to the last bit of the scores).  On either side of the border, 8 heads
+// of 2048, forward and backward: d = 64, 1392 keys 531 and 936 us, the general kernels at 1400
+// keys 1891 and 1577; d = 128, 1072 keys 624 and 1474, 1080 keys 2815 and 2832; d = 32, 1584 keys
+// 377 and 655, 1585 keys 1283 and 1403.  Smaller windows: d = 64, 1000 keys 307 and 840, 512 keys
+// 177 and 593, 256 keys 111 and 386.
 bool win_f32_fits(int window, int sinks, int d) {
     const int cols = win_cols(window, sinks);
     const size_t sm = d == 128 ? win_smem<128>(cols, 2, 2) : d == 64 ? win_smem<64>(cols, 2, 2) : win_smem<32>(cols, 2, 2);

@@ -260,3 +260,20 @@ def test_a_query_that_is_no_number(bad, dtype, kw):
         assert not bool(a[0, 1, r].any())      # (a NaN is true)
         a[0, 1, r] = b[0, 1, r]
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("d,most", [(32, 1584), (64, 1392), (128, 1072)])
+@pytest.mark.parametrize("sinks", [0, 130])
+def test_both_sides_of_the_shared_memory_border(d, most, sinks):
+    """The largest float32 window whose scores fit in shared memory and the next one; the counters tell the routes
+    apart (the general kernels visit their blocks again in every pass)."""
+    N = most + 270
+    q, k, v, do = make(1, 1, N, d, "f32", 13)
+    for window, general in ((most - sinks, False), (most + 1 - sinks, True)):
+        ws = A.workspace(1 << 22, q.device)
+        A.entmax_attn_fwd(q, k, v, 1.5, True, window=window, sinks=sinks, ws=ws)
+        visited, weighed, passes, _ = A.read_status(ws)[:4]
+        assert passes > 0 and (visited > weighed) == general
+        want = reference(q, k, v, do, 1.5, window, sinks)
+        for delta in ("otilde", "recompute"):
+            check(grads_of(q, k, v, do, 1.5, window, sinks, delta), want, "f32", v)
