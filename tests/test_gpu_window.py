@@ -277,3 +277,92 @@ def test_both_sides_of_the_shared_memory_border(d, most, sinks):
         want = reference(q, k, v, do, 1.5, window, sinks)
         for delta in ("otilde", "recompute"):
             check(grads_of(q, k, v, do, 1.5, window, sinks, delta), want, "f32", v)
+
+
+@pytest.mark.parametrize("dtype,window,sinks", [("f32", 600, 130), ("f32", 1500, 4), ("bf16", 600, 130),
+                                                ("bf16", 1500, 4), ("bf16", 4299, 0)])
+def test_gradients_over_many_tiles(dtype, window, sinks):
+    """34 query tiles: more than dkv looks at in one step."""
+    q, k, v, do = make(1, 1, 4300, 64, dtype, 14)
+    want = reference(q, k, v, do, 1.5, window, sinks)
+    for delta in ("otilde", "recompute"):
+        check(grads_of(q, k, v, do, 1.5, window, sinks, delta), want, dtype, v)
+
+
+@pytest.mark.parametrize("delta", ["otilde", "recompute"])
+@pytest.mark.parametrize("dtype,N,window,sinks", [("f32", 400, 150, 8), ("f32", 1700, 1500, 4), ("bf16", 400, 150, 8),
+                                                  ("bf16", 900, 257, 130)])
+@pytest.mark.parametrize("alpha", [1.7, 2.0])
+def test_gradients_where_g_is_steep(alpha, dtype, N, window, sinks, delta):
+    """alpha above 1.6: g = u^(gamma-1) jumps or is steep at the border of the support, so a key whose score lies
+    within its rounding of tau may be in or out.  The formula is taken at the kernel's own tau, and rows with such a
+    key get dO = 0, which leaves dS = 0 whatever g is: the others are held to the bounds of the smooth case.  A
+    score's rounding: sums of d products in float, 2^-24 of sum |q k| for each (the tensor core's truncation twice
+    that), and a rounding of x and of tau."""
+    B, H, d = 1, 2, 64
+    q, k, v, do = make(B, H, N, d, dtype, 15)
+    ot = torch.empty(q.shape, device="cuda") if delta == "otilde" else None
+    o, tau, mask, _ = A.entmax_attn_fwd(q, k, v, alpha, True, otilde=ot, window=window, sinks=sinks)
+    q6, k6, v6 = (t.double() for t in (q, k, v))
+    gamma, scale, seen = 1 / (alpha - 1), d ** -0.5, visible(N, window, sinks)
+    x = (alpha - 1) * scale * (q6 @ k6.transpose(-1, -2))
+    u = x - tau.double()[..., None]
+    off = 2 * d * 2.0 ** -24 * (alpha - 1) * scale * (q6.abs() @ k6.abs().transpose(-1, -2))
+    off = off + 2.0 ** -23 * (x.abs() + tau.double().abs()[..., None])
+    unsure = ((u.abs() <= off) & seen).any(-1)
+    assert float(unsure.double().mean()) < 0.1
+    do = do.masked_fill(unsure[..., None], 0)
+    u = torch.where(seen, u, -1.0).clamp_min(0)
+    g = torch.where(u > 0, u ** (gamma - 1), 0.0)
+    dp = do.double() @ v6.transpose(-1, -2)
+    ds = g * (dp - (g * dp).sum(-1, keepdim=True) / g.sum(-1, keepdim=True)) * scale
+    got = A.entmax_attn_bwd(q, k, v, None if delta == "otilde" else o, do, tau, mask, alpha, True, otilde=ot,
+                            window=window, sinks=sinks)
+    want = (ds @ k6, ds.transpose(-1, -2) @ q6, (u ** gamma).transpose(-1, -2) @ do.double())
+    for name, a, b in zip(("dq", "dk", "dv"), got, want):
+        rel = float((a.double() - b).norm() / b.norm())
+        assert rel <= GRAD[dtype], f"{name} off by {rel:.3g}"
+
+
+@pytest.mark.parametrize("delta", ["otilde", "recompute"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_one_visible_key_has_no_gradient_of_scores(dtype, delta):
+    """window 1: dS = g (dP - delta) with dP = delta but for rounding, d products of 2^-22 of sum |dO v| at most
+    (g = 1 within 1e-4), and dQ and dK are that times one key or query."""
+    q, k, v, do = make(1, 2, 515, 64, dtype, 16)
+    got = grads_of(q, k, v, do, 1.5, 1, 0, delta)
+    ds = 64 * 2.0 ** -22 * (do.double().abs() * v.double().abs()).sum(-1, keepdim=True) * 64 ** -0.5 * 1.01
+    assert bool((got[1].double().abs() <= ds * k.double().abs()).all())
+    assert bool((got[2].double().abs() <= ds * q.double().abs()).all())
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_work_grows_with_the_window_not_with_the_sequence(d):
+    """A pass of a tile visits its visible blocks and at most the two of a job that was started early."""
+    N, W, S = 4000, 256, 3
+    q, k, v, _ = make(1, 2, N, d, "bf16", 17)
+    ws = A.workspace(1 << 24, q.device)
+    A.entmax_attn_fwd(q, k, v, 1.5, True, window=W, sinks=S, ws=ws)
+    visited, _, passes, tiles = A.read_status(ws)[:4]
+    assert tiles == 2 * 32 and visited <= (passes + tiles) * (4 + 2)
+    A.entmax_attn_fwd(q, k, v, 1.5, True, ws=ws)
+    assert A.read_status(ws)[0] > 2 * visited
+
+
+@pytest.mark.parametrize("N,d,window,sinks,alpha", [(2000, 64, 512, 4, 1.5), (1500, 128, 300, 130, 1.25),
+                                                    (9000, 64, 700, 0, 1.5)])
+@pytest.mark.parametrize("otilde", [False, True])
+def test_tiles_solved_again(N, d, window, sinks, alpha, otilde, monkeypatch):
+    """With a tolerance that every unevaluated stop misses, tiles are solved again by whichever CTA is free: the bits
+    of evaluated stops."""
+    q, k, v, _ = make(1, 3, N, d, "bf16", 18)
+    runs = []
+    for name, value in (("ENTATTN_VERIFY_TOL", "-1"), ("ENTATTN_ACCEPT", "0")):
+        with monkeypatch.context() as m:
+            m.setenv(name, value)
+            ws = A.workspace(1 << 26, q.device)
+            ot = torch.empty(q.shape, device="cuda") if otilde else None
+            out = A.entmax_attn_fwd(q, k, v, alpha, True, with_iters=True, otilde=ot, window=window, sinks=sinks, ws=ws)
+            runs.append((A.read_status(ws)[3], *out, *([ot] if otilde else [])))
+    assert runs[0][0] > runs[1][0] == 3 * -(-N // 128)
+    assert all(torch.equal(a, b) for a, b in zip(runs[0][1:], runs[1][1:]))
