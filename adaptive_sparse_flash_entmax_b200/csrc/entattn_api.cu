@@ -771,7 +771,10 @@ bool kv4_layout(const ent::Kv4Geom& g, long long rows, int group, int d, int dty
     l->chunk = ent::kv4_chunk_keys(l->block);
     l->nchunk = ent::kv4_chunks(g, l->chunk);
     // runs: a warp each, enough of them for two rounds of 16 on each SM and no more (a longer
-    // run pays its prologue once, and a higher maximum filters its later chunks)
+    // run pays its prologue once, and a higher maximum filters its later chunks).  16 are resident
+    // where four rows share a warp; 12 or 8 for more rows, which so take up to four rounds.  Two
+    // rounds of those measured better and worse: eight rows of 32 / 8 heads, 4 x 8192, 51 us
+    // instead of 61, in float32 59 instead of 67, but 16 x 16384 in float32 330 instead of 300.
     const long long items = per > 0 ? rows / per * l->blocks : 0;
     long long want = items > 0 ? (2 * 16 * 148 + items - 1) / items : 1;
     if (want > ent::kKvMaxRuns) want = ent::kKvMaxRuns;
