@@ -196,7 +196,9 @@ def entmax_attn_kv4(q, cache, block_table, start, alpha: float = 1.5, *, new_len
     Row l of sequence b, at position i = start[b] + l, sees key j when j <= i and, with a ``window``,
     i - j < window or j < sinks; rows from new_lens[b] on give zeros.  Query head h reads key head
     h // (Hq // Hkv).  ``max_len`` bounds start + new_lens (default: what the table covers) and sizes
-    the workspace; ``tau`` (float32 [B, Hq, L]) also takes the rows' thresholds; ``bad`` as in
+    the workspace, 8 bytes for each query row and token of that cover (of window + sinks + L under a
+    window): give it where the table covers much more than the sequences hold, and few rows a call
+    where they are long; ``tau`` (float32 [B, Hq, L]) also takes the rows' thresholds; ``bad`` as in
     ``kv4_write``.  No gradient."""
     _check_rows4(q)
     B, Hq, L, d = q.shape

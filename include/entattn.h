@@ -398,8 +398,12 @@ ent_status ent_entmax_rows_bwd(const void *z, const float *tau, const void *dp, 
  * see no key (their pages missing) give zeros (tau 0); rows with a NaN or an infinite
  * score give NaN.  tau (nullable) float [B][Hq][L], in units of x, absolute.  max_len (at
  * most max_pages * page) bounds start + new_lens and sizes the workspace,
- * ent_attn_kv4_workspace_size (0 for sizes the call refuses); a workspace belongs to one
- * call at a time.  The result does not depend on what else runs, and is the same from
+ * ent_attn_kv4_workspace_size (0 for sizes the call refuses): 8 bytes for each query row and
+ * token of the cover (under a window, of window + sinks + L), since every key may be a
+ * candidate: 134 MB for one token of 16 sequences, 32 heads and a cover of 32768, beside a
+ * cache of 671 MB for 8 key heads of 128, and 1 GB for 512 rows of 32 heads over 8192.  A
+ * max_len near the lengths keeps it small; long prompts want calls of fewer rows.  A workspace
+ * belongs to one call at a time.  The result does not depend on what else runs, and is the same from
  * call to call.
  *
  * Limits: d in {32, 64, 128}, B * Hkv <= 65535, max_pages * page <= 2^30, 1 < alpha <= 2, window, sinks >= 0
