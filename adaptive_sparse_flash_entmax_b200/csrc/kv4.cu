@@ -988,9 +988,14 @@ __global__ void __launch_bounds__(kSolveThreads, 4) kv4_solve_kernel(const Kv4Ar
                 }
                 mine += __popc(mask);
             }, [&] {
-                if (lane == 0 && mine > told) atomicAdd(&found, mine - told);
+                // (one lane reads: the warp must go on or stop as one)
+                int all = 0;
+                if (lane == 0) {
+                    if (mine > told) atomicAdd(&found, mine - told);
+                    all = *const_cast<volatile int*>(&found);
+                }
                 told = mine;
-                return *const_cast<volatile int*>(&found) > kCap;
+                return __shfl_sync(kFull, all, 0) > kCap;
             });
         };
         __syncthreads();
@@ -1017,8 +1022,8 @@ __global__ void __launch_bounds__(kSolveThreads, 4) kv4_solve_kernel(const Kv4Ar
     // so on (with the dense weights of alpha 1.25 the first drops nine candidates of ten).  What
     // decides is the count above m - 1, which the keys alone determine; how many entries the lists
     // hold besides is a matter of timing, and deciding by that number, though it spares a row of
-    // many entries the first look (sixteen sequences of 32768 at alpha 1.25 take 362 us, not 354;
-    // of 16384 with 4300 a row above m - 1 115, not 158), changed last bits from call to call.
+    // many entries the first look (sixteen sequences of 32768 at alpha 1.25 take 366 us, not 354;
+    // of 16384 with 4300 a row above m - 1 116, not 158), changed last bits from call to call.
     float bound = -1.f;
     int total = 0;
     bool fits;
