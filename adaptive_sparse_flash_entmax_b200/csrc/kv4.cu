@@ -11,7 +11,7 @@
 // below such a maximum - 1 has p = 0: the scores never leave the chip but for the few that
 // can weigh, and value rows without a weight are never read.
 //
-// 16 sequences of 16k to 32k tokens, 32 query and 8 key heads of 128 (B200): 104 us a call for
+// 16 sequences of 16k to 32k tokens, 32 query and 8 key heads of 128 (B200): 99 us a call for
 // 253 MB of keys and weighed values, 39 at the copy rate; the scores kernel takes 78 of them,
 // bound by its instructions (half of the issue slots at four warps a scheduler; matrix pipe
 // 22 %, 3.2 TB/s), the solver the rest after it.
