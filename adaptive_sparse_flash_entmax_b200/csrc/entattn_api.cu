@@ -402,6 +402,9 @@ ent_status bwd_impl(const void* q, const void* k, const void* v, const float* ot
     if (win.want) {
         a.window = win.window < N ? win.window : N;
         a.sinks = win.sinks < N ? win.sinks : N;
+        // every query sees one key, whose weight is 1 whatever its score: dQ and dK are zero, not
+        // what rounding leaves of dP - delta (dV is as ever)
+        if (a.window == 1 && a.sinks == 0) a.scale = 0.f;
     }
     if (lists.want) {
         a.list_key = lists.key; a.list_u = lists.u; a.list_n = lists.n;

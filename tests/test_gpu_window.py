@@ -366,3 +366,14 @@ def test_tiles_solved_again(N, d, window, sinks, alpha, otilde, monkeypatch):
             runs.append((A.read_status(ws)[3], *out, *([ot] if otilde else [])))
     assert runs[0][0] > runs[1][0] == 3 * -(-N // 128)
     assert all(torch.equal(a, b) for a, b in zip(runs[0][1:], runs[1][1:]))
+
+
+@pytest.mark.parametrize("delta", ["otilde", "recompute"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("alpha,N,d", [(1.25, 24, 32), (1.5, 515, 64), (2.0, 300, 128)])
+def test_one_visible_key_exactly(alpha, N, d, dtype, delta):
+    """window 1 without sinks: dQ and dK are zeros, dV is dO but for p's own error (test_forward_and_gradients)."""
+    q, k, v, do = make(2, 3, N, d, dtype, 19, beta=4.0)
+    _, dq, dk, dv = grads_of(q, k, v, do, alpha, 1, 0, delta)
+    assert not bool(dq.any()) and not bool(dk.any())
+    assert float((dv.double() - do.double()).norm()) <= GRAD[dtype] * float(do.double().norm())
