@@ -377,3 +377,23 @@ def test_one_visible_key_exactly(alpha, N, d, dtype, delta):
     _, dq, dk, dv = grads_of(q, k, v, do, alpha, 1, 0, delta)
     assert not bool(dq.any()) and not bool(dk.any())
     assert float((dv.double() - do.double()).norm()) <= GRAD[dtype] * float(do.double().norm())
+
+
+@pytest.mark.parametrize("B,H,N,d,window,sinks,alpha,beta", [(1, 8, 24, 128, 10, 0, 1.5, 4.0), (2, 8, 30, 64, 12, 2, 1.5, 4.0),
+                                                             (1, 8, 257, 64, 64, 4, 1.5, 1.0), (1, 8, 300, 32, 90, 4, 1.25, 2.0)])
+def test_float32_is_as_near_as_float_scores(B, H, N, d, window, sinks, alpha, beta):
+    """O's error (2-norm) is that of the exact entmax of float32 scores and at most 5e-7 beside it: |sum p - 1| <= 4e-7,
+    a factor of a row's p, and two roundings of 2^-24 (p and the sum)."""
+    q, k, v, _ = make(B, H, N, d, "f32", 20, beta)
+    o = entmax_attention(q, k, v, alpha, True, window=window, sinks=sinks).double()
+    want = forward64(q.double(), k.double(), v.double(), alpha, window, sinks)[0]
+    assert not torch.backends.cuda.matmul.allow_tf32
+    x = ((q @ k.transpose(-1, -2)) * ((alpha - 1) / d ** 0.5)).double().masked_fill(~visible(N, window, sinks), float("-inf"))
+    hi = x.amax(-1, keepdim=True)
+    lo = hi - 1
+    for _ in range(56):
+        mid = (lo + hi) / 2
+        up = torch.relu(x - mid).pow(1 / (alpha - 1)).sum(-1, keepdim=True) > 1
+        lo, hi = torch.where(up, mid, lo), torch.where(up, hi, mid)
+    plain = torch.relu(x - (lo + hi) / 2).pow(1 / (alpha - 1)) @ v.double()
+    assert float((o - want).norm()) <= float((plain - want).norm()) + 5e-7 * float(want.norm())
